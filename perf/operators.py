@@ -170,7 +170,8 @@ def _quantise(x, g):
     y = x * (1.0 / g)[:, None, None]
     y = y.unflatten(-1, (-1, 16))
     a = y.abs()
-    s = (a.amax(-1) / 6.0).clamp_max(448.0).to(torch.float8_e4m3fn)
+    six = torch.full((), 6.0, device=x.device)      # a tensor: a true division
+    s = (a.amax(-1) / six).clamp_max(448.0).to(torch.float8_e4m3fn)
     t = s.float().unsqueeze(-1)
     code = torch.zeros(y.shape, dtype=torch.uint8, device=x.device)
     for bound, tie_up in ((0.25, False), (0.75, True), (1.25, False), (1.75, True), (2.5, False),
