@@ -1,0 +1,719 @@
+// Split-KV attention over a 4-bit cache for few query rows (GBSA, ReSA summary
+// §3.4.1 Eq. 2 over a block list, or Eq. 1 over every position): up to 16 query
+// rows of one kv head (a group's heads, or the heads of a few chunk rows) read
+// each 4-bit key and value once.
+//
+// Work.  A unit is a (sequence, kv head) with its list of blocks.  The blocks
+// of all units form one line of W entries, and CTA c of G takes entries
+// [cW/G, (c+1)W/G): every CTA gets the same share whatever the lengths, and its
+// share is a run of pieces, each one unit's.  A unit inside one CTA is written
+// directly; of a unit that spans several, each CTA stores a partial (o, max,
+// sum) and the last to arrive, counted by a ticket it resets, adds them up in
+// CTA order, so the result does not depend on the arrival order.
+//
+// Inside a piece, warp w takes every eighth step of 32 positions (two tiles of
+// 16) through a private cp.async ring of kStages steps and keeps its own
+// online softmax; the warps' states are merged at the end of the piece.
+//
+// The MMAs are m16n8k16 fp16 with the operands swapped, S^T = K Q^T and
+// O^T = V^T P^T, so the query rows sit on the N = 8 side.  The contraction index
+// may be permuted freely as long as both operands agree, and so may O's
+// channels, so that a lane's MMA fragments are the codes of one contiguous run:
+//   K: lane (r, c) = (lane / 4, lane % 4) takes channels c * D/4 .. of tokens r
+//      and r + 8; MMA k-step s uses its channels 4s .. 4s+3;
+//   V: lane (r, c) takes channels r * D/8 .. of tokens 2c, 2c+1, 2c+8, 2c+9, and
+//      pairs up the two tokens of a register with byte permutes.
+// c * s is exact in fp16.  q is scaled by a power of two per row into fp16's
+// range (its 8 bits stay exact), and P enters as fp16 hi + lo (22 bits) scaled
+// by 2^kShift, so the products lose nothing that fp32 accumulation keeps.
+#include "q4_common.cuh"
+
+namespace resa {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 4;
+constexpr int kStep = 32;          // positions a warp takes at a time
+constexpr int kMinBlocks = 4;      // blocks a CTA takes at least, when there are few
+constexpr float kShift = 13.f;     // P is stored as 2^kShift * exp2(x - m)
+constexpr float kSlack = 2.f;      // growth of the maximum tolerated before rescaling
+
+template <int D>
+struct Q4Smem {
+    static constexpr int kCodes = kTileRows * D / 2;   // one tile's K or V codes
+    static constexpr int kScales = kTileRows * D / 16; // and group scales
+    static constexpr int kV = 2 * kCodes;              // offsets inside a stage (two tiles)
+    static constexpr int kKs = 4 * kCodes;
+    static constexpr int kVs = kKs + 2 * kScales;
+    static constexpr int kStage = kVs + 2 * kScales;
+    static constexpr int kRing = kWarps * kStages * kStage;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack_f16(a, b);
+    lo = pack_f16(a - f16_lo(hi), b - f16_hi(hi));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float pow2i(int k) {  // 2^k, k in [-126, 127]
+    return __int_as_float((127 + k) << 23);
+}
+
+// Byte offset of (token t, 8-byte piece p) of a V code tile: the 16-byte chunks
+// of a 128-byte line are XORed with its index, so that the eight lanes of a
+// quarter-warp phase (four token pairs, two neighbouring pieces) meet all banks.
+template <int D>
+__device__ __forceinline__ uint32_t v_chunk(int t, int chunk) {
+    constexpr int kPerRow = D / 32;         // 16-byte chunks a row
+    constexpr int kRowsPerLine = 8 / kPerRow;
+    const int line = t / kRowsPerLine, slot = (t % kRowsPerLine) * kPerRow + chunk;
+    return (uint32_t)(line * 128 + ((slot ^ ((line & 3) * 2)) << 4));
+}
+
+__device__ __forceinline__ void cp_async16_s(uint32_t smem_dst, const void *gsrc) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
+}
+// Shared-memory loads of 1, 2 or 4 consecutive words, and of a byte or two.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr));
+    return x;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t x;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr));
+    return x;
+}
+
+struct Unit {
+    int b, h, row, L, n, cnt;  // cnt: blocks to take, 0 when there is nothing to do
+    bool live;                 // outputs are written (else they stay as they were)
+};
+
+struct DecodeQ4Args {
+    Q4Cache c;
+    const int32_t *page_table, *seq_len, *n_new, *block_idx, *block_cnt;
+    const uint16_t *q;
+    float *part_o, *out, *lse;
+    float2 *part_ml;
+    uint32_t *tickets, *err;
+    RowMap rm;
+    int f, row0, max_topk, batch, hq, hkv, g, max_pages, num_pages, bs;
+    float scale_log2;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
+    using SM = Q4Smem<D>;
+    constexpr int kWords = D / 32;   // 32-bit words of codes a lane takes per K row
+    constexpr int kRows = NT * 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long sh_sum[kWarps + 1];
+    __shared__ int sh_unit;
+    __shared__ long long sh_first;
+    __shared__ uint32_t sh_last;
+
+    pdl_launch_next();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r = lane >> 2, c = lane & 3;
+    const int units = a.batch * a.hkv;
+    const int cta = blockIdx.x;
+
+    // Unit u: its row, length, fresh tokens and number of blocks.
+    auto unit_of = [&](int u, bool report) -> Unit {
+        Unit x;
+        x.b = u / a.hkv;
+        x.h = u - x.b * a.hkv;
+        x.n = a.n_new ? a.n_new[x.b] : a.f;
+        x.cnt = 0;
+        x.L = 0;
+        x.row = -1;
+        x.live = !a.n_new || x.n != 0;
+        if (!x.live) return x;
+        uint32_t *err = report && x.h == 0 ? a.err : nullptr;
+        x.row = cache_row(a.rm, x.b, err);
+        x.L = row_seq_len(a.seq_len, x.row);
+        const bool dense = a.block_idx == nullptr;
+        if (x.row < 0 || x.L < (dense ? 0 : 1) || (long long)x.L > (long long)a.max_pages * a.bs) {
+            set_error(err, RESA_DEVERR_SEQ_LEN);
+            x.live = !dense;
+            return x;
+        }
+        if (dense) {
+            if (x.n < 0 || x.n > a.f || x.n > x.L) {
+                set_error(err, RESA_DEVERR_CHUNK);
+                x.live = false;
+                return x;
+            }
+            // rows row0 .. row0 + 15 of the chunk see positions below lim
+            const int rows = min(x.n * a.g - a.row0, kMaxGroup);
+            if (rows <= 0) {
+                x.live = false;
+                return x;
+            }
+            const int lim = x.L - x.n + (a.row0 + rows - 1) / a.g + 1;
+            x.cnt = (lim + a.bs - 1) / a.bs;
+        } else {
+            x.cnt = max(0, min(a.block_cnt[u], a.max_topk + 1));
+        }
+        return x;
+    };
+
+    // Prefix sums of the units' blocks: thread t sums units [t * per, ...).
+    const int per = (units + kThreads - 1) / kThreads;
+    const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
+    long long mine = 0;
+    for (int u = u_lo; u < u_hi; ++u) mine += unit_of(u, false).cnt;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh_sum[warp] = incl;
+    __syncthreads();
+    long long before = 0, W = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sh_sum[w];
+        W += sh_sum[w];
+    }
+    incl += before;
+    // CTAs that take work: at least kMinBlocks entries each
+    const long long G = max(1LL, min((long long)gridDim.x, (W + kMinBlocks - 1) / kMinBlocks));
+    const long long x0 = cta < G ? W * cta / G : W, x1 = cta < G ? W * (cta + 1) / G : W;
+    if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
+        long long s = incl - mine;
+        for (int u = u_lo; u < u_hi; ++u) {
+            const int k = unit_of(u, false).cnt;
+            if (x0 < s + k) {
+                sh_unit = u;
+                sh_first = s;
+                break;
+            }
+            s += k;
+        }
+    }
+    __syncthreads();
+
+    int u = x0 < x1 ? sh_unit : 0;
+    long long ustart = x0 < x1 ? sh_first : 0;
+    const int sub_shift = a.bs == 64 ? 2 : a.bs == 32 ? 1 : 0;  // tiles a block
+    uint8_t *ring = smem + (size_t)warp * kStages * SM::kStage;
+    const uint32_t ring_s = smem_u32(ring);
+
+    for (long long x = x0; x < x1; ++u) {
+        const Unit un = unit_of(u, false);
+        if (un.cnt == 0) continue;
+        const long long uend = ustart + un.cnt;
+        const int j0 = (int)(x - ustart), j1 = (int)(min(x1, uend) - ustart);  // entries of this piece
+        const int b = un.b, h = un.h, L = un.L;
+        const int rows_all = a.block_idx ? a.g : min(un.n * a.g - a.row0, kMaxGroup);
+        const int base_pos = a.block_idx ? 0 : L - un.n;  // row rho sees positions <= base_pos + rho / g
+        const int nblk_seq = (L + a.bs - 1) / a.bs;
+        const int32_t *list =
+            a.block_idx ? a.block_idx + (size_t)u * (a.max_topk + 1) : nullptr;
+        const int32_t *pages = a.page_table + (size_t)un.row * a.max_pages;
+
+        // This warp's steps: tiles 2p, 2p + 1 of the piece for p = warp + kWarps t.
+        const int ntiles = (j1 - j0) << sub_shift;
+        const int npairs = (ntiles + 1) >> 1;
+        const int nsteps = warp < npairs ? (npairs - warp + kWarps - 1) / kWarps : 0;
+        // Tiles' places 16 steps at a time, one a lane (lane 2i + k: tile k of
+        // step 16 w + i), with the next window already in flight: byte-tile
+        // index of the cache (page, head, tile in block), position, validity.
+        auto load_win = [&](int w, long long &tile, int &pos) {
+            const int t = w * 16 + (lane >> 1);
+            const int e = 2 * (warp + kWarps * t) + (lane & 1);
+            tile = -1;
+            pos = 0;
+            if (t >= nsteps || e >= ntiles) return;
+            const int j = j0 + (e >> sub_shift), sub = e & ((1 << sub_shift) - 1);
+            const int blk = list ? list[j] : j;
+            if (blk < 0 || blk >= nblk_seq) {
+                set_error(a.err, RESA_DEVERR_BLOCK);
+                return;
+            }
+            pos = blk * a.bs + sub * kTileRows;
+            if (pos >= L) return;
+            const int page = pages[blk];
+            if (page < 0 || page >= a.num_pages) {
+                set_error(a.err, RESA_DEVERR_PAGE);
+                return;
+            }
+            tile = ((((long long)page * a.hkv + h) << sub_shift) | sub);
+        };
+        long long win_tile[2];
+        int win_pos[2];
+        load_win(0, win_tile[0], win_pos[0]);
+        load_win(1, win_tile[1], win_pos[1]);
+        // The loads of step t (its window is 0 or 1 ahead of the consumer's).
+        int win_base = 0;  // window held in slot 0
+        auto tile_at = [&](int t, int k, int &pos) -> long long {
+            const int w = (t >> 4) - win_base, src = 2 * (t & 15) + k;
+            const long long t0 = __shfl_sync(0xffffffffu, win_tile[0], src);
+            const long long t1 = __shfl_sync(0xffffffffu, win_tile[1], src);
+            const int p0 = __shfl_sync(0xffffffffu, win_pos[0], src);
+            const int p1 = __shfl_sync(0xffffffffu, win_pos[1], src);
+            pos = w ? p1 : p0;
+            return w ? t1 : t0;
+        };
+        auto issue = [&](int t) {
+            if (t < nsteps) {
+                const uint32_t st = ring_s + (uint32_t)(t % kStages) * SM::kStage;
+                constexpr int kChunks = SM::kCodes / 16;  // 16-byte chunks of a code tile
+                constexpr int kPerRow = D / 32;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    int pos;
+                    const long long tile = tile_at(t, k, pos);
+                    if (tile < 0) continue;
+                    const uint8_t *gk = a.c.k + (size_t)tile * SM::kCodes;
+                    const uint8_t *gv = a.c.v + (size_t)tile * SM::kCodes;
+#pragma unroll
+                    for (int i = 0; i < kChunks / 32; ++i) {
+                        const int q = lane + 32 * i;
+                        cp_async16_s(st + k * SM::kCodes + q * 16, gk + q * 16);
+                        cp_async16_s(st + SM::kV + k * SM::kCodes + v_chunk<D>(q / kPerRow, q % kPerRow),
+                                     gv + q * 16);
+                    }
+                    constexpr int kSc = SM::kScales / 16;  // chunks of a scale tile
+                    if (lane < 2 * kSc) {
+                        const bool is_v = lane >= kSc;
+                        const int q = is_v ? lane - kSc : lane;
+                        cp_async16_s(st + (is_v ? SM::kVs : SM::kKs) + k * SM::kScales + q * 16,
+                                     (is_v ? a.c.v_sf : a.c.k_sf) + (size_t)tile * SM::kScales + q * 16);
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int t = 0; t < kStages - 1; ++t) issue(t);
+
+        // Q^T fragments and each row's factors.
+        uint32_t qb[D / 16][NT][2];
+        float row_scale[NT][2];
+        int lim[NT][2];  // positions row 2c + k of n-tile n sees (0: no such row)
+        const float kg = head_scale(a.c.k_scale, h);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int rho = n * 8 + r;
+            const bool ok = rho < rows_all;
+            const int qr = a.row0 + (ok ? rho : 0);
+            const size_t qrow = ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow * D + c * (D / 4));
+            uint4 x[D / 32];
+            uint32_t mag = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                x[i] = ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+                mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                             __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+            }
+            mag = max(mag & 0xffffu, mag >> 16);
+            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 1));
+            mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, 2));
+            // largest |q| to [2^8, 2^9); zero and non-finite rows keep factor 1
+            int e = 0;
+            if (mag != 0 && mag < 0x7f80u) e = max(-110, min(119, (int)(mag >> 7) - 127 - 8));
+            const float f2 = pow2i(-e);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    qb[2 * i + k][n][0] = pack_f16(bf_lo(w[2 * k]) * f2, bf_hi(w[2 * k]) * f2);
+                    qb[2 * i + k][n][1] = pack_f16(bf_lo(w[2 * k + 1]) * f2, bf_hi(w[2 * k + 1]) * f2);
+                }
+            }
+            const float sc = a.scale_log2 * kg * pow2i(e);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = n * 8 + 2 * c + k;
+                row_scale[n][k] = __shfl_sync(0xffffffffu, sc, (2 * c + k) * 4);
+                lim[n][k] = row >= rows_all ? 0
+                            : a.block_idx   ? L
+                                            : base_pos + (a.row0 + row) / a.g + 1;
+            }
+        }
+        const int lim_all = a.block_idx ? L : base_pos + a.row0 / a.g + 1;  // every row sees these
+
+        float m[NT][2], l[NT][2], o[D / 16][NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.f;
+        }
+
+        for (int t = 0; t < nsteps; ++t) {
+            int tp[2];
+            bool there[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) there[k] = tile_at(t, k, tp[k]) >= 0;
+            issue(t + kStages - 1);
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const uint32_t st = ring_s + (uint32_t)(t % kStages) * SM::kStage;
+            // positions of the tiles that any row sees (0 .. 16), and whether all rows see all
+            int ntok[2];
+            bool masked = false;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                ntok[k] = there[k] ? min(kTileRows, L - tp[k]) : 0;
+                masked |= !there[k] || tp[k] + kTileRows > lim_all;
+            }
+            float s[2][NT][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[k][n][0] = s[k][n][1] = s[k][n][2] = s[k][n][3] = 0.f;
+                const uint32_t kt = st + k * SM::kCodes;
+                uint32_t w[2][kWords];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) lds_words<kWords>(w[i], kt + (r + 8 * i) * (D / 2) + c * (D / 8));
+                uint32_t sc[2][D / 64];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t at = st + SM::kKs + k * SM::kScales + (r + 8 * i) * (D / 16) + c * (D / 64);
+                    if (D == 128) {
+                        const uint32_t p = e4m3x2_to_f16(lds_u16(at));
+                        sc[i][0] = __byte_perm(p, p, 0x1010);
+                        sc[i][D / 64 - 1] = __byte_perm(p, p, 0x3232);
+                    } else {
+                        const uint32_t p = e4m3x2_to_f16(lds_u8(at));
+                        sc[i][0] = __byte_perm(p, p, 0x1010);
+                    }
+                }
+#pragma unroll
+                for (int wi = 0; wi < kWords; ++wi) {
+                    uint32_t e0[4], e1[4];
+                    e2m1x8_to_f16(w[0][wi], e0);
+                    e2m1x8_to_f16(w[1][wi], e1);
+                    const int gi = wi / 2;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        e0[j] = mul_f16x2(e0[j], sc[0][gi]);
+                        e1[j] = mul_f16x2(e1[j], sc[1][gi]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma_f16(s[k][n], e0[2 * j], e1[2 * j], e0[2 * j + 1], e1[2 * j + 1],
+                                    qb[2 * wi + j][n][0], qb[2 * wi + j][n][1]);
+                }
+            }
+            // Softmax over the step's 32 positions, per query row (column).
+            uint32_t bh[2][NT][2], bl[2][NT][2];
+            bool grow = false;
+            float mt[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh) {
+                                const int pos = tp[k] + r + 8 * hh;
+                                if (!there[k] || pos >= lim[n][k2]) s[k][n][2 * hh + k2] = -INFINITY;
+                            }
+                    }
+                    float x = fmaxf(fmaxf(s[0][n][k2], s[0][n][2 + k2]), fmaxf(s[1][n][k2], s[1][n][2 + k2]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    mt[n][k2] = x * row_scale[n][k2];
+                    grow |= mt[n][k2] > m[n][k2] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float alpha[2];
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        // a whole number, so that every factor 2^(m - m') is exact
+                        const float mn = ceilf(fmaxf(m[n][k2], mt[n][k2]));
+                        alpha[k2] = m[n][k2] == -INFINITY ? 0.f : ex2(m[n][k2] - mn);
+                        m[n][k2] = mn;
+                        l[n][k2] *= alpha[k2];
+                    }
+#pragma unroll
+                    for (int t2 = 0; t2 < D / 16; ++t2) {
+                        o[t2][n][0] *= alpha[0];
+                        o[t2][n][1] *= alpha[1];
+                        o[t2][n][2] *= alpha[0];
+                        o[t2][n][3] *= alpha[1];
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float nb[2];
+#pragma unroll
+                for (int k2 = 0; k2 < 2; ++k2) nb[k2] = m[n][k2] == -INFINITY ? 0.f : kShift - m[n][k2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = ex2(fmaf(s[k][n][e], row_scale[n][e & 1], nb[e & 1]));
+                    l[n][0] += p[0] + p[2];
+                    l[n][1] += p[1] + p[3];
+                    uint32_t h0, l0, h1, l1;
+                    split_f16(p[0], p[1], h0, l0);
+                    split_f16(p[2], p[3], h1, l1);
+                    bh[k][n][0] = movmatrix_trans(h0);
+                    bh[k][n][1] = movmatrix_trans(h1);
+                    bl[k][n][0] = movmatrix_trans(l0);
+                    bl[k][n][1] = movmatrix_trans(l1);
+                }
+            }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t vt = st + SM::kV + k * SM::kCodes;
+                uint32_t sv[2];  // scales of the token pairs (2c, 2c+1), (2c+8, 2c+9)
+                uint32_t w[4][D / 64];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t0 = 2 * c + 8 * i;
+                    const uint32_t at = st + SM::kVs + k * SM::kScales + t0 * (D / 16) + r * D / 128;
+                    uint32_t s0 = lds_u8(at), s1 = lds_u8(at + D / 16);
+                    if (masked) {  // whatever the slots past the end hold, their values count as 0
+                        s0 = t0 < ntok[k] ? s0 : 0u;
+                        s1 = t0 + 1 < ntok[k] ? s1 : 0u;
+                    }
+                    sv[i] = e4m3x2_to_f16(s0 | (s1 << 8));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int t1 = t0 + j;
+                        if (D == 128)
+                            lds_words<D / 64>(w[2 * i + j], vt + v_chunk<D>(t1, r >> 1) + (r & 1) * 8);
+                        else
+                            lds_words<D / 64>(w[2 * i + j], vt + v_chunk<D>(t1, r >> 2) + (r & 3) * 4);
+                    }
+                }
+#pragma unroll
+                for (int wi = 0; wi < D / 64; ++wi) {
+                    uint32_t e[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e2m1x8_to_f16(w[i][wi], e[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a0 = mul_f16x2(__byte_perm(e[0][j], e[1][j], 0x5410), sv[0]);
+                        const uint32_t a1 = mul_f16x2(__byte_perm(e[0][j], e[1][j], 0x7632), sv[0]);
+                        const uint32_t a2 = mul_f16x2(__byte_perm(e[2][j], e[3][j], 0x5410), sv[1]);
+                        const uint32_t a3 = mul_f16x2(__byte_perm(e[2][j], e[3][j], 0x7632), sv[1]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16(o[4 * wi + j][n], a0, a1, a2, a3, bh[k][n][0], bh[k][n][1]);
+                            mma_f16(o[4 * wi + j][n], a0, a1, a2, a3, bl[k][n][0], bl[k][n][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if ((t & 15) == 15) {  // window 0 is used up
+                win_tile[0] = win_tile[1];
+                win_pos[0] = win_pos[1];
+                ++win_base;
+                load_win(win_base + 1, win_tile[1], win_pos[1]);
+            }
+        }
+        cp_async_wait<0>();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+                l[n][k2] += __shfl_xor_sync(0xffffffffu, l[n][k2], 4);
+                l[n][k2] += __shfl_xor_sync(0xffffffffu, l[n][k2], 8);
+                l[n][k2] += __shfl_xor_sync(0xffffffffu, l[n][k2], 16);
+            }
+        __syncthreads();  // every ring is drained
+        // Merge the warps: states to shared memory, [warp][row] and [warp][row][D].
+        float *wm = reinterpret_cast<float *>(smem);
+        float *wl = wm + kWarps * kRows;
+        float *wo = wl + kWarps * kRows;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+                const int rho = n * 8 + 2 * c + k2;
+                if (r == 0) {
+                    wm[warp * kRows + rho] = m[n][k2];
+                    wl[warp * kRows + rho] = l[n][k2];
+                }
+                float *dst = wo + ((size_t)warp * kRows + rho) * D + r * (D / 8);
+#pragma unroll
+                for (int t2 = 0; t2 < D / 16; ++t2)
+                    *reinterpret_cast<float2 *>(dst + 2 * t2) = make_float2(o[t2][n][k2], o[t2][n][2 + k2]);
+            }
+        __syncthreads();
+        const bool whole = j0 == 0 && j1 == un.cnt;
+        const float vg = head_scale(a.c.v_scale, h);
+        const float kLn2 = 0.6931471805599453f;
+        auto orow_of = [&](int rho) -> size_t {
+            const int qr = a.row0 + rho;
+            return ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
+        };
+        // partial slot of CTA q for this unit: 2q when its share starts in the
+        // unit (its first piece), else 2q + 1 (its last piece)
+        auto slot_of = [&](long long q) -> size_t {
+            return (size_t)(2 * q + (W * q / G >= ustart ? 0 : 1));
+        };
+        const size_t slot = whole ? 0 : slot_of(cta);
+        for (int e = tid; e < rows_all * D; e += kThreads) {
+            const int rho = e / D, ch = e % D;
+            float ms = -INFINITY, ls = 0.f, os = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) ms = fmaxf(ms, wm[w * kRows + rho]);
+            if (ms != -INFINITY) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f2 = ex2(wm[w * kRows + rho] - ms);
+                    ls += wl[w * kRows + rho] * f2;
+                    os += wo[((size_t)w * kRows + rho) * D + ch] * f2;
+                }
+            }
+            if (whole) {
+                const size_t orow = orow_of(rho);
+                a.out[orow * D + ch] = ls > 0.f ? os / ls * vg : 0.f;
+                if (a.lse && ch == 0)
+                    a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2 : -INFINITY;
+            } else {
+                a.part_o[(slot * kMaxGroup + rho) * D + ch] = os;
+                if (ch == 0) a.part_ml[slot * kMaxGroup + rho] = make_float2(ms, ls);
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            // CTAs whose shares meet the unit
+            const long long q0 = ((ustart + 1) * G - 1) / W, q1 = (uend * G - 1) / W;
+            if (tid == 0) {
+                const uint32_t k = atomicAdd(&a.tickets[u], 1u);
+                sh_last = k == (uint32_t)(q1 - q0);
+                if (sh_last) a.tickets[u] = 0u;
+            }
+            __syncthreads();
+            if (sh_last) {
+                __threadfence();
+                for (int e = tid; e < rows_all * D; e += kThreads) {
+                    const int rho = e / D, ch = e % D;
+                    float ms = -INFINITY, ls = 0.f, os = 0.f;
+                    for (long long q = q0; q <= q1; ++q)
+                        ms = fmaxf(ms, __ldcg(&a.part_ml[slot_of(q) * kMaxGroup + rho]).x);
+                    if (ms != -INFINITY)
+                        for (long long q = q0; q <= q1; ++q) {
+                            const size_t sl = slot_of(q) * kMaxGroup + rho;
+                            const float2 ml = __ldcg(&a.part_ml[sl]);
+                            const float f2 = ex2(ml.x - ms);
+                            ls += ml.y * f2;
+                            os += __ldcg(&a.part_o[sl * D + ch]) * f2;
+                        }
+                    const size_t orow = orow_of(rho);
+                    a.out[orow * D + ch] = ls > 0.f ? os / ls * vg : 0.f;
+                    if (a.lse && ch == 0)
+                        a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();  // the merge area is the ring again
+        x = min(x1, uend);
+        ustart = uend;
+    }
+
+    // Units without any block: zeros and -inf, and the errors of every unit.
+    for (int u = cta; u < units; u += gridDim.x) {
+        const Unit x = unit_of(u, tid == 0);
+        if (x.cnt > 0 || !x.live) continue;
+        const size_t o = (size_t)x.b * a.f * a.hq + (size_t)x.h * a.g;  // sparse: f = 1
+        for (int e = tid; e < a.g * D; e += kThreads) a.out[o * D + e] = 0.f;
+        if (a.lse && tid < a.g) a.lse[o + tid] = -INFINITY;
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch_t(const DecodeQ4Args &a, int ctas, cudaStream_t st) {
+    constexpr int merge = kWarps * NT * 8 * (D + 2) * 4;
+    constexpr int smem = Q4Smem<D>::kRing > merge ? Q4Smem<D>::kRing : merge;
+    static std::atomic<int> done[64];
+    cudaError_t e = ensure_smem(decode_q4_kernel<D, NT>, smem, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(decode_q4_kernel<D, NT>, dim3(ctas), dim3(kThreads), smem, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
+                             const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
+                             int row0, const int32_t *block_idx, const int32_t *block_cnt,
+                             int max_topk, int sms, float *part_o, float *part_ml,
+                             uint32_t *tickets, float *out, float *lse, uint32_t *err,
+                             cudaStream_t st) {
+    DecodeQ4Args a{};
+    a.c = c;
+    a.page_table = page_table;
+    a.seq_len = seq_len;
+    a.n_new = n_new;
+    a.block_idx = block_idx;
+    a.block_cnt = block_cnt;
+    a.q = static_cast<const uint16_t *>(q);
+    a.part_o = part_o;
+    a.out = out;
+    a.lse = lse;
+    a.part_ml = reinterpret_cast<float2 *>(part_ml);
+    a.tickets = tickets;
+    a.err = err;
+    a.rm = s.rows;
+    a.f = f;
+    a.row0 = row0;
+    a.max_topk = max_topk;
+    a.batch = s.batch;
+    a.hq = s.hq;
+    a.hkv = s.hkv;
+    a.g = s.g;
+    a.max_pages = s.max_pages;
+    a.num_pages = s.num_pages;
+    a.bs = s.bs;
+    a.scale_log2 = s.sm_scale * 1.4426950408889634f;
+    // one CTA per SM; two partial slots a CTA in the decode partials
+    const int ctas = sms < kNumSms ? sms : kNumSms;
+    const int rows = block_idx ? s.g : (f * s.g - row0 < kMaxGroup ? f * s.g - row0 : kMaxGroup);
+    if (s.d == 128) return rows <= 8 ? launch_t<128, 1>(a, ctas, st) : launch_t<128, 2>(a, ctas, st);
+    return rows <= 8 ? launch_t<64, 1>(a, ctas, st) : launch_t<64, 2>(a, ctas, st);
+}
+
+}  // namespace resa

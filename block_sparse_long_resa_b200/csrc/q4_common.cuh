@@ -1,0 +1,137 @@
+// The 4-bit cache format (resa_cache_q4_t): 16 channels of a token and kv head
+// share an e4m3 scale s, a channel is an e2m1 code c, and c * s is exact in
+// fp16 (2 + 4 significant bits, magnitudes 2^-10 .. 2688), which is what the
+// attention kernels feed their MMAs with.  The head's fp32 scale g is folded
+// into the softmax scale (keys) and into the output (values).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "resa_common.cuh"
+
+namespace resa {
+
+constexpr int kQ4Group = 16;  // channels a group scale covers
+
+// The pointers of a resa_cache_q4_t the kernels take.
+struct Q4Cache {
+    uint8_t *k, *v, *k_sf, *v_sf;
+    const float *k_scale, *v_scale;
+};
+
+__device__ __forceinline__ float head_scale(const float *g, int h) { return g ? g[h] : 1.f; }
+
+// Eight codes (channels c .. c+7, low nibble first) to four fp16 pairs.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+}
+// Two e4m3 bytes (low byte first) to an fp16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+// Nearest e4m3 (ties to even, saturating at 448) of a non-negative value.
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+    return r & 0xffu;
+}
+__device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
+    const uint32_t h = e4m3x2_to_f16(byte);
+    return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float f16_lo(uint32_t p) {
+    return __half2float(__ushort_as_half((unsigned short)(p & 0xffffu)));
+}
+__device__ __forceinline__ float f16_hi(uint32_t p) {
+    return __half2float(__ushort_as_half((unsigned short)(p >> 16)));
+}
+
+// Quantise one group x[0..15] with 1/g = rg: codes (channel i in nibble i) and
+// the e4m3 scale byte.  The code of y is the number of e2m1 decision points
+// t * s it passes; t * s is exact in fp32 (3 + 4 bits), so no quotient y / s is
+// rounded and ties go to the even code, as e2m1's nearest-even does.  NaN
+// counts as 0 and infinity saturates; returns whether either occurred.
+__device__ __forceinline__ bool q4_quantise(const float (&x)[kQ4Group], float rg, uint2 &codes,
+                                            uint32_t &sf) {
+    float y[kQ4Group], amax = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < kQ4Group; ++i) {
+        y[i] = x[i] * rg;
+        amax = fmaxf(amax, fabsf(y[i]));
+        finite = finite && (fabsf(y[i]) < INFINITY);
+    }
+    sf = f32_to_e4m3(__fdiv_rn(amax, 6.f));
+    const float s = e4m3_to_f32(sf);
+    codes = make_uint2(0u, 0u);
+    if (s > 0.f) {
+        const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s,
+                    t5 = 3.5f * s, t6 = 5.f * s;
+#pragma unroll
+        for (int i = 0; i < kQ4Group; ++i) {
+            const float a = fabsf(y[i]);
+            uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
+            c |= y[i] < 0.f ? 8u : 0u;
+            if (i < 8)
+                codes.x |= c << (4 * i);
+            else
+                codes.y |= c << (4 * (i - 8));
+        }
+    }
+    return !finite;
+}
+
+// Eight channels as bf16: c * s * g, rounded once.
+__device__ __forceinline__ uint4 q4_values_bf16(uint32_t word, uint32_t sf, float g) {
+    uint32_t e[4];
+    e2m1x8_to_f16(word, e);
+    const float s = e4m3_to_f32(sf);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // c * s is exact in fp32
+        o[i] = pack_bf16(f16_lo(e[i]) * s * g, f16_hi(e[i]) * s * g);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Arguments of the rotary append kernels.
+struct AppendArgs {
+    void *k, *v, *k_sf, *v_sf, *desc;   // k_sf, v_sf: 4-bit cache only
+    const float *k_scale, *v_scale;
+    const void *q, *kn, *vn;
+    void *q_out;
+    long long q_stride, k_stride, v_stride;  // elements
+    const int32_t *page_table, *seq_len, *n_new, *positions;
+    const float *inv_freq;
+    double mscale;
+    int f, rot, interleaved;
+};
+cudaError_t launch_append_rope(const Shape &s, const AppendArgs &a, bool q4, uint32_t *err,
+                               cudaStream_t st);
+cudaError_t launch_expand_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
+                             const int32_t *seq_len, void *k_out, void *v_out, uint32_t *err,
+                             cudaStream_t st);
+// Split-KV attention over a 4-bit cache.  block_idx == nullptr: every position
+// (query rows f, row r of n sees positions 0 .. L - n + r); else the listed
+// blocks (f = 1).  At most kMaxGroup rows f * g from row row0 on.
+cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
+                             const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
+                             int row0, const int32_t *block_idx, const int32_t *block_cnt,
+                             int max_topk, int sms, float *part_o, float *part_ml,
+                             uint32_t *tickets, float *out, float *lse, uint32_t *err,
+                             cudaStream_t st);
+
+}  // namespace resa

@@ -20,6 +20,7 @@ STATUS_NAMES = {0: "RESA_OK", 1: "RESA_ERR_NULL", 2: "RESA_ERR_SHAPE", 3: "RESA_
                 4: "RESA_ERR_UNSUPPORTED", 5: "RESA_ERR_CUDA", 6: "RESA_ERR_DEVICE_CHECK"}
 DEVERR_SEQ_LEN, DEVERR_PAGE, DEVERR_BLOCK, DEVERR_TOPK, DEVERR_CHUNK, DEVERR_TIMEOUT, DEVERR_ROW = (
     0x1, 0x2, 0x4, 0x8, 0x10, 0x20, 0x40)
+DEVERR_NONFINITE = 0x80
 
 
 class ResaError(RuntimeError):
@@ -44,6 +45,28 @@ class resa_cache_t(ctypes.Structure):
                 ("table_rows", ctypes.c_int32)]
 
 
+class resa_cache_q4_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
+                ("v_sf", ctypes.c_void_p), ("desc", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("rows", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class resa_rope_t(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_float)]
+
+
+class resa_tokens_t(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("f", ctypes.c_int32),
+                ("n_new", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -64,6 +87,12 @@ _SIGS = {
                          ctypes.c_int),
     "resa_sparse_decode_noalloc": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _P], ctypes.c_int),
     "resa_dense_decode": ([_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "resa_append_rope": ([_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "resa_append_rope_q4": ([_P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "resa_expand_q4": ([_P, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "resa_sparse_decode_q4": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, ctypes.c_size_t, _P],
+                              ctypes.c_int),
+    "resa_attention_q4": ([_P, _P, _I, _P, _P, _P, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "resa_kernels_per_call": ([ctypes.c_char_p], ctypes.c_int32),
     "resa_decode_step_launches": ([_P, _I, _I, _I], ctypes.c_int32),
     "resa_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -130,6 +159,55 @@ def make_cache(k, v, desc, page_table, seq_len, rows=None) -> resa_cache_t:
     return resa_cache_t(_ptr(k), _ptr(v), _ptr(desc), _ptr(page_table), _ptr(seq_len),
                         int(rows.numel()), int(page_table.shape[1]), int(k.shape[0]),
                         _ptr(rows), nrows)
+
+
+def _keep(struct, *tensors):
+    """The struct holds addresses only: keep its small tensors alive with it."""
+    struct.tensors = tensors
+    return struct
+
+
+def make_cache_q4(k, k_sf, v, v_sf, desc, page_table, seq_len, rows=None, k_scale=None,
+                  v_scale=None) -> resa_cache_q4_t:
+    """4-bit cache struct over torch tensors k/v [pages][Hkv][b][d/2] uint8 codes, k_sf/v_sf
+    [pages][Hkv][b][d/16] float8_e4m3fn group scales, desc / page_table / seq_len / rows as in
+    make_cache, and the heads' scales k_scale/v_scale [Hkv] fp32 (None: 1)."""
+    nrows = int(page_table.shape[0])
+    return _keep(resa_cache_q4_t(_ptr(k), _ptr(v), _ptr(k_sf), _ptr(v_sf), _ptr(desc),
+                                 _ptr(page_table), _ptr(seq_len),
+                                 nrows if rows is None else int(rows.numel()),
+                                 int(page_table.shape[1]), int(k.shape[0]), _ptr(rows),
+                                 0 if rows is None else nrows, _ptr(k_scale), _ptr(v_scale)),
+                 rows, k_scale, v_scale)
+
+
+def make_rope(rot_dim: int, inv_freq, interleaved: bool = False,
+              mscale: float = 1.0) -> resa_rope_t:
+    """Rotary embedding of the first ``rot_dim`` channels; inv_freq: fp32 device tensor
+    [rot_dim / 2] (None when rot_dim is 0)."""
+    return _keep(resa_rope_t(rot_dim, 1 if interleaved else 0,
+                             _ptr(inv_freq) if rot_dim else None, mscale), inv_freq)
+
+
+def _token_stride(t, name: str) -> int:
+    """Elements between consecutive tokens of a [batch][f][heads][d] tensor."""
+    if t.dim() != 4:
+        raise ResaError(2, f"make_tokens: {name} is not [batch][f][heads][d]")
+    b, f, h, d = t.shape
+    tok = t.stride(1) if f > 1 else (t.stride(0) if b > 1 else h * d)
+    if (tok < h * d or (d > 1 and t.stride(3) != 1) or (h > 1 and t.stride(2) != d)
+            or (b > 1 and f > 1 and t.stride(0) != f * tok)):
+        raise ResaError(4, f"make_tokens: {name} is not evenly strided by tokens")
+    return tok
+
+
+def make_tokens(q, k, v, n_new=None, positions=None) -> resa_tokens_t:
+    """Fresh tokens of a call: q [batch][f][Hq][d] (or None), k, v [batch][f][Hkv][d] bf16, e.g.
+    views of one fused projection output; n_new [batch] and positions [batch][f] int32 or None."""
+    return _keep(resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),
+                               0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"),
+                               _token_stride(v, "v"), int(k.shape[1]), _ptr(n_new),
+                               _ptr(positions)), q, k, v, n_new, positions)
 
 
 # ---------------------------------------------------------------------------
@@ -217,6 +295,46 @@ def resa_sparse_decode_noalloc(cfg, cache, q, block_idx, block_cnt, max_topk: in
                                             _ptr(block_idx), _ptr(block_cnt), max_topk, _ptr(out),
                                             _ptr(lse), _ptr(dev_error), _stream(stream)),
            "resa_sparse_decode_noalloc")
+
+
+def resa_append_rope(cfg, cache, rope, tokens, q_out, ws, stream=None):
+    """Append fresh tokens to the bf16 cache, queries and keys rotated on the way."""
+    _check(lib().resa_append_rope(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
+                                  ctypes.byref(tokens), _ptr(q_out), _ptr(ws), ws.numel(),
+                                  _stream(stream)),
+           "resa_append_rope")
+
+
+def resa_append_rope_q4(cfg, cache, rope, tokens, q_out, ws, stream=None):
+    """resa_append_rope into a 4-bit cache (make_cache_q4)."""
+    _check(lib().resa_append_rope_q4(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
+                                     ctypes.byref(tokens), _ptr(q_out), _ptr(ws), ws.numel(),
+                                     _stream(stream)),
+           "resa_append_rope_q4")
+
+
+def resa_expand_q4(cfg, cache, k_out, v_out, ws, stream=None):
+    """Write a 4-bit cache's valid positions into bf16 pages k_out / v_out."""
+    _check(lib().resa_expand_q4(ctypes.byref(cfg), ctypes.byref(cache), _ptr(k_out), _ptr(v_out),
+                                _ptr(ws), ws.numel(), _stream(stream)),
+           "resa_expand_q4")
+
+
+def resa_sparse_decode_q4(cfg, cache, q, block_idx, block_cnt, max_topk: int, out, lse, ws,
+                          stream=None):
+    """resa_sparse_decode over a 4-bit cache."""
+    _check(lib().resa_sparse_decode_q4(ctypes.byref(cfg), ctypes.byref(cache), _ptr(q),
+                                       _ptr(block_idx), _ptr(block_cnt), max_topk, _ptr(out),
+                                       _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "resa_sparse_decode_q4")
+
+
+def resa_attention_q4(cfg, cache, f: int, n_new, q, out, lse, ws, stream=None):
+    """Causal attention of each sequence's last n_new (None: f) tokens over its 4-bit cache."""
+    _check(lib().resa_attention_q4(ctypes.byref(cfg), ctypes.byref(cache), f, _ptr(n_new),
+                                   _ptr(q), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                   _stream(stream)),
+           "resa_attention_q4")
 
 
 def resa_kernels_per_call(entry_point: str) -> int:

@@ -88,6 +88,7 @@ typedef enum {
 #define RESA_DEVERR_CHUNK 0x10u    /* rectification chunk f > seq_len */
 #define RESA_DEVERR_TIMEOUT 0x20u  /* a bounded device wait gave up */
 #define RESA_DEVERR_ROW 0x40u      /* rows[i] outside [0, table_rows): sequence skipped */
+#define RESA_DEVERR_NONFINITE 0x80u /* NaN or infinity appended to a 4-bit cache: stored as a finite value */
 
 typedef struct {
     int32_t num_q_heads;   /* Hq */
@@ -121,6 +122,68 @@ typedef struct {
     const int32_t *rows;        /* row map [batch], device, or NULL (see above) */
     int32_t table_rows;         /* rows of page_table / seq_len when rows != NULL */
 } resa_cache_t;
+
+/* 4-bit cache of one attention layer.  The 16 channels 16j .. 16j+15 of one
+ * token and kv head form a group: with the head's scale g (k_scale / v_scale)
+ * and y = x * (1 / g), the group's scale is s = e4m3(max |y| / 6) and each
+ * channel is stored as c = e2m1(y / s) (both to nearest even, saturating), which
+ * stands for c * s * g.  c * s is exact in 16 bits.  Of a value that is not
+ * finite, NaN is stored as 0 and infinity as the largest value (with
+ * RESA_DEVERR_NONFINITE); group scales are finite.
+ *   k, v          [num_pages][Hkv][b][d / 2] bytes: channel 2j in the low and
+ *                 2j+1 in the high four bits of byte j (e2m1: sign, 2 exponent
+ *                 bits, 1 mantissa bit)
+ *   k_sf, v_sf    [num_pages][Hkv][b][d / 16] e4m3
+ *   k_scale, v_scale  [Hkv] fp32, device, positive; NULL: 1
+ *   desc, page_table, seq_len, rows, table_rows: as in resa_cache_t; desc holds
+ *                 the min / max of the keys as stored, rounded to bf16.
+ * resa_select_blocks takes such a cache's descriptors: give it a resa_cache_t
+ * with the same desc, page_table, seq_len and sizes and any non-NULL k.  Slots
+ * at positions >= seq_len are never read and may hold anything. */
+typedef struct {
+    void *k;                    /* 4-bit codes, device */
+    void *v;
+    void *k_sf;                 /* group scales, device */
+    void *v_sf;
+    void *desc;                 /* [num_pages][Hkv][2][d] bf16, device */
+    const int32_t *page_table;  /* [rows][max_pages], device */
+    const int32_t *seq_len;     /* [rows], device; counts the call's fresh tokens */
+    int32_t batch;
+    int32_t max_pages;
+    int32_t num_pages;
+    const int32_t *rows;        /* row map or NULL */
+    int32_t table_rows;
+    const float *k_scale;       /* [Hkv], device, or NULL */
+    const float *v_scale;
+} resa_cache_q4_t;
+
+/* Rotary position embedding.  Channels 0 .. rot_dim-1 of every query and key
+ * head are rotated in pairs, the others are copied: with the token's position t
+ * and a_i = t * inv_freq[i], pair i becomes
+ *   (x1 cos a_i - x2 sin a_i, x2 cos a_i + x1 sin a_i) * mscale.
+ * The angle is reduced in 64 bits, so far positions lose nothing; keys are
+ * rotated in 64 bits and queries in 32, each rounded once to bf16. */
+typedef struct {
+    int32_t rot_dim;       /* 0 .. d, a multiple of 16; 0: no rotation */
+    int32_t interleaved;   /* 0: pair i = channels (i, i + rot_dim/2); 1: (2i, 2i+1) */
+    const float *inv_freq; /* [rot_dim / 2], device (NULL when rot_dim is 0) */
+    float mscale;          /* factor on cos and sin; 0 selects 1 */
+} resa_rope_t;
+
+/* Fresh tokens of a call: sequence i brings n_new[i] tokens (0 .. f; rows
+ * n_new[i] .. f-1 of its arrays are padding), which take the cache positions
+ * seq_len - n_new[i] .. seq_len - 1 (seq_len counts them already). */
+typedef struct {
+    const void *q;            /* [batch][f][Hq][d] bf16, or NULL: no queries */
+    const void *k;            /* [batch][f][Hkv][d] bf16 */
+    const void *v;            /* [batch][f][Hkv][d] bf16 */
+    int64_t q_stride;         /* elements from a token to the next (f tokens a sequence); */
+    int64_t k_stride;         /*   0: contiguous; a multiple of 8, e.g. the row length of */
+    int64_t v_stride;         /*   a fused projection's output */
+    int32_t f;                /* tokens a sequence, padding included; >= 1 */
+    const int32_t *n_new;     /* [batch], device, or NULL: f each */
+    const int32_t *positions; /* [batch][f], device: positions of the rotation, or NULL: the cache's */
+} resa_tokens_t;
 
 /* Bytes of workspace needed for caches of `batch` sequences with up to
  * `max_pages` blocks each and rectification chunks of up to `max_chunk`
@@ -269,11 +332,71 @@ RESA_API resa_status_t resa_sparse_decode_noalloc(const resa_config_t *cfg,
                                                   float *out, float *lse_opt,
                                                   uint32_t *dev_error, cudaStream_t stream);
 
+/* Append fresh tokens to the bf16 cache with the rotary embedding applied on
+ * the way (Algorithm 1, "Incremental cache updates", for any number of tokens:
+ * a prompt, a chunk, or one decode token):
+ *   - rotate the queries into q_out [batch][f][Hq][d] bf16 (contiguous; may be
+ *     tokens->q itself when that is contiguous; NULL exactly when tokens->q is);
+ *   - rotate the keys and write keys and values at their positions;
+ *   - rebuild the descriptors of the blocks that hold fresh tokens, over their
+ *     positions < seq_len (the cached keys of a partly filled block included).
+ * Rows of padding are not read and stay as they were in q_out.  A sequence with
+ * n_new = 0 is skipped whatever its length; n_new outside 0 .. f or above
+ * seq_len sets RESA_DEVERR_CHUNK and the sequence is skipped.  A block whose
+ * page is out of range sets RESA_DEVERR_PAGE and is skipped.  One launch. */
+RESA_API resa_status_t resa_append_rope(const resa_config_t *cfg, const resa_cache_t *cache,
+                                        const resa_rope_t *rope, const resa_tokens_t *tokens,
+                                        void *q_out, void *ws, size_t ws_bytes,
+                                        cudaStream_t stream);
+
+/* The same into a 4-bit cache: keys are rotated, rounded to bf16 and then
+ * stored in 4 bits; the descriptors hold the min / max of the keys as stored.
+ * One launch. */
+RESA_API resa_status_t resa_append_rope_q4(const resa_config_t *cfg, const resa_cache_q4_t *cache,
+                                           const resa_rope_t *rope, const resa_tokens_t *tokens,
+                                           void *q_out, void *ws, size_t ws_bytes,
+                                           cudaStream_t stream);
+
+/* Expand a 4-bit cache into bf16 pages: k_out, v_out [num_pages][Hkv][b][d]
+ * bf16 (the k, v of a resa_cache_t with the same page table, lengths and
+ * descriptors).  Positions 0 .. seq_len-1 of the call's sequences are written
+ * (values c * s * g rounded once to bf16), all others stay as they were.  A
+ * sequence of length 0 is skipped.  One launch. */
+RESA_API resa_status_t resa_expand_q4(const resa_config_t *cfg, const resa_cache_q4_t *cache,
+                                      void *k_out, void *v_out, void *ws, size_t ws_bytes,
+                                      cudaStream_t stream);
+
+/* Group block-sparse attention over a 4-bit cache: resa_sparse_decode with the
+ * same arguments and the same treatment of block lists.  A (sequence, kv head)
+ * with block_cnt 0 gives out = 0 and lse = -inf.  One launch. */
+RESA_API resa_status_t resa_sparse_decode_q4(const resa_config_t *cfg,
+                                             const resa_cache_q4_t *cache, const void *q,
+                                             const int32_t *block_idx, const int32_t *block_cnt,
+                                             int32_t max_topk, float *out, float *lse_opt,
+                                             void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Causal attention of each sequence's last tokens over every position of a
+ * 4-bit cache that holds them already (resa_append_rope_q4): query row r of
+ * q [batch][f][Hq][d] bf16 (position L - n + r, L = seq_len, n = n_new_opt[i] or
+ * f) attends to positions 0 .. L - n + r.  f = 1 is the dense decode step, f > 1
+ * the attention of a prompt chunk or of a rectification (ReSA summary §3.4.2).
+ * out [batch][f][Hq][d] fp32, lse_opt (nullable) [batch][f][Hq] fp32, natural
+ * log.  Rows r >= n are padding: not read, and left as they were in out and lse.
+ * A sequence with n = 0 is skipped whatever its length; n outside 0 .. f or
+ * above L sets RESA_DEVERR_CHUNK and the sequence is skipped.
+ * f must be 1 or in 1 .. max_chunk of the workspace, and f * g at most 16384
+ * (more: RESA_ERR_UNSUPPORTED).  One launch. */
+RESA_API resa_status_t resa_attention_q4(const resa_config_t *cfg, const resa_cache_q4_t *cache,
+                                         int32_t f, const int32_t *n_new_opt, const void *q,
+                                         float *out, float *lse_opt, void *ws, size_t ws_bytes,
+                                         cudaStream_t stream);
+
 /* Number of kernels each entry point launches per call (for launch
  * accounting): 1 for append and build, 2 for select, 1 for sparse decode,
  * 2 for rectify, 1 for a decode step of the fused shapes (see
  * resa_decode_step_launches for the others), 1 for the no-allocation decode,
- * 1 for the dense decode.
+ * 1 for the dense decode, 1 for each rotary append, 4-bit expansion and 4-bit
+ * attention.
  * Unknown names return -1. */
 RESA_API int32_t resa_kernels_per_call(const char *entry_point);
 
