@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libresa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 SOURCES = ["resa_api.cu", "desc_kernels.cu", "select_kernels.cu", "decode_kernel.cu",
            "rectify_tc.cu", "decode_noalloc.cu", "step_kernel.cu", "append_rope.cu",
-           "decode_q4.cu", "q4_api.cu"]
+           "decode_q4.cu", "chunk_q4_tc.cu", "q4_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden"]

@@ -1,0 +1,756 @@
+// Causal attention of a chunk of query rows over a 4-bit cache on the
+// 5th-generation tensor cores (ReSA summary §3.4.2; prompt chunks): more than 16
+// query rows of one (sequence, kv head).
+//
+// Rows of one (sequence, kv head) are rho = r * g + j (chunk row r, group head j),
+// taken 256 at a time (a row group: two M = 128 tiles, m = 0 and 1).  A unit is
+// (sequence, kv head, row group) with its tiles of 128 keys.  The tiles of all
+// units form one line of W entries; CTA c of G takes [cW/G, (c+1)W/G), a run of
+// pieces, each one unit's.  A unit inside one CTA is written directly; of a
+// unit that spans several, each stores its partial (o, max, sum), and after a
+// bounded grid barrier (cooperative launch, one CTA per SM) those CTAs merge an
+// equal share of its rows, in CTA order.
+//
+// Warp roles (384 threads; registers moved from warpgroup 0 to the others):
+//   warp 0      TMEM owner and MMA issuer (one thread);
+//   warps 1-3   bring the 4-bit tiles in (cp.async, three raw stages) and expand
+//               them, c * s in fp16 (exact), into 128-byte swizzled operand tiles:
+//               a ring of three 32 KB slots K0 V0 K1 V1 ..;
+//   warps 4-7, 8-11   softmax of M tile 0 and 1, one thread a row.
+// Per M tile the chain is QK^T(i) -> softmax -> P V(i) -> QK^T(i+1); the two M
+// tiles run half a period apart, so one's MMAs fill the other's softmax.
+//
+// Precision.  q enters as fp16 scaled per row by a power of two (its 8 bits stay
+// exact), so Q K^T has exact products.  P enters as fp16 hi + lo (22 bits), both
+// over the tile's S in tensor memory, 32 keys (16 + 16 columns) at a time.  The
+// matrix unit truncates when it adds to its fp32 accumulator, which over a long
+// sequence would be a bias of 10^-5, so P V starts from zero at every tile and
+// the softmax thread adds the tile's O to its row in registers (fused with the
+// rescaling, o = o * 2^(m - m') + tile), where additions round to nearest.
+#include "q4_common.cuh"
+#include "tc_common.cuh"
+
+namespace resa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = kRectRowsPerCta;  // 256
+constexpr int kKeys = 128;              // keys per tile
+constexpr int kSlots = 3;               // fp16 operand tiles
+constexpr int kRaw = 3;                 // 4-bit tiles in flight
+constexpr int kConv = 96;               // converter threads
+constexpr int kMinTiles = 2;            // tiles a CTA takes at least, when there are few
+constexpr float kShift = 13.f;          // P is stored as 2^kShift * exp2(x - m)
+
+template <int D>
+struct ChunkSmem {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalf = 128 * 128;          // 128 rows of 64 channels
+    static constexpr int kTile = kHalves * kHalf;    // one M tile of Q, or K or V
+    static constexpr int kCodes = kKeys * D / 2;
+    static constexpr int kScales = kKeys * D / 16;
+    static constexpr int kRawStage = 2 * (kCodes + kScales);  // K codes, V codes, K and V scales
+    static constexpr int kSlotOff = 2 * kTile;
+    static constexpr int kRawOff = kSlotOff + kSlots * kTile;
+    static constexpr int kBytes = kRawOff + kRaw * kRawStage + 1024;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void conv_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
+
+// Byte offset of 16-byte chunk c of row r of a raw code tile: within a 128-byte
+// line the chunks are XORed so that eight consecutive rows' chunks c meet all banks.
+template <int D>
+__device__ __forceinline__ uint32_t raw_chunk(int r, int c) {
+    constexpr int kPerRow = D / 32, kRowsPerLine = 8 / kPerRow;
+    const int line = r / kRowsPerLine;
+    return (uint32_t)(line * 128 + ((r % kRowsPerLine) * kPerRow + (c ^ (line & (kPerRow - 1)))) * 16);
+}
+
+struct ChunkArgs {
+    Q4Cache c;
+    const int32_t *page_table, *seq_len, *n_new;
+    const uint16_t *q;
+    float *part_o, *out, *lse;
+    float2 *part_ml;
+    unsigned long long *grid_bar;
+    uint32_t *err;
+    RowMap rm;
+    int f, batch, hkv, g, groups, max_pages, num_pages, bs;
+    float scale_log2;
+};
+
+// One CTA's run through the line of tiles.
+struct Piece {
+    int b, h, row, L, n;
+    int row0, rows;   // first query row of the unit's group, rows of it
+    int cnt, t0, t1;  // the unit's tiles, this piece's
+    int ustart;       // the unit's first entry
+    int slot;         // partial slot of the CTA: 0 for its first piece
+};
+
+struct UnitInfo {
+    int b, h, row, L, n, row0, rows, cnt;
+};
+__device__ __forceinline__ UnitInfo chunk_unit(const ChunkArgs &a, int u, uint32_t *err) {
+    UnitInfo x;
+    const int rg = u % a.groups, bh = u / a.groups;
+    x.b = bh / a.hkv;
+    x.h = bh - x.b * a.hkv;
+    x.n = a.n_new ? a.n_new[x.b] : a.f;
+    x.cnt = x.rows = x.L = 0;
+    x.row = -1;
+    x.row0 = rg * kRows;
+    if (x.n == 0) return x;
+    if (x.h != 0 || rg != 0) err = nullptr;
+    x.row = cache_row(a.rm, x.b, err);
+    x.L = row_seq_len(a.seq_len, x.row);
+    if (x.row < 0 || x.L < 0 || (long long)x.L > (long long)a.max_pages * a.bs) {
+        set_error(err, RESA_DEVERR_SEQ_LEN);
+        return x;
+    }
+    if (x.n < 0 || x.n > a.f || x.n > x.L) {
+        set_error(err, RESA_DEVERR_CHUNK);
+        return x;
+    }
+    x.rows = min(kRows, x.n * a.g - x.row0);
+    if (x.rows <= 0) {
+        x.rows = 0;
+        return x;
+    }
+    const int lim = x.L - x.n + (x.row0 + x.rows - 1) / a.g + 1;  // keys the last row sees
+    x.cnt = (lim + kKeys - 1) / kKeys;
+    return x;
+}
+
+// First entry of CTA q's share.
+__device__ __forceinline__ int entry_of(int q, int W, int G) {
+    return q < G ? (int)((long long)W * q / G) : W;
+}
+
+struct Walk {
+    int x, x1, ustart, u, slot;
+    __device__ __forceinline__ bool next(const ChunkArgs &a, Piece &p) {
+        while (x < x1) {
+            const UnitInfo i = chunk_unit(a, u++, nullptr);
+            if (i.cnt > 0) {
+                p.b = i.b;
+                p.h = i.h;
+                p.row = i.row;
+                p.L = i.L;
+                p.n = i.n;
+                p.row0 = i.row0;
+                p.rows = i.rows;
+                p.cnt = i.cnt;
+                p.ustart = ustart;
+                p.slot = slot;
+                slot = 1;
+                p.t0 = x - ustart;
+                ustart += i.cnt;
+                x = min(x1, ustart);
+                p.t1 = x - p.ustart;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_q4_kernel(const __grid_constant__ ChunkArgs a) {
+    using SM = ChunkSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    __shared__ uint64_t q_ready[2], slot_full[kSlots], slot_free[kSlots], s_full[2], p_full[2];
+    __shared__ uint32_t tmem_base_s, sh_ok;
+    __shared__ uint32_t tile_mask[4];  // valid 16-key blocks of a tile
+    __shared__ int sh_sum[kThreads / 32], sh_w, sh_ctas, sh_first, sh_unit;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int units = a.batch * a.hkv * a.groups;
+    const int cta = blockIdx.x;
+
+    // This CTA's share of the line: prefix sums of the units' tiles.
+    const int per = (units + kThreads - 1) / kThreads;
+    const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
+    int mine = 0;
+    for (int u = u_lo; u < u_hi; ++u) mine += chunk_unit(a, u, nullptr).cnt;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh_sum[warp] = incl;
+    if (tid == 0) {
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&slot_full[s], kConv);
+            mbar_init(&slot_free[s], 1);
+        }
+        for (int m = 0; m < 2; ++m) {
+            mbar_init(&q_ready[m], 128);
+            mbar_init(&s_full[m], 1);
+            mbar_init(&p_full[m], 128);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 0) tc::tmem_alloc(&tmem_base_s, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_base_s;
+    {
+        int W = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) incl += sh_sum[w];
+            W += sh_sum[w];
+        }
+        const int G = max(1, min((int)gridDim.x, (W + kMinTiles - 1) / kMinTiles));
+        if (tid == 0) {
+            sh_w = W;
+            sh_ctas = G;
+        }
+        const int x0 = entry_of(cta, W, G);
+        if (x0 < entry_of(cta + 1, W, G) && incl - mine <= x0 && x0 < incl) {
+            int s = incl - mine;
+            for (int u = u_lo; u < u_hi; ++u) {
+                const int k = chunk_unit(a, u, nullptr).cnt;
+                if (x0 < s + k) {
+                    sh_unit = u;
+                    sh_first = s;
+                    break;
+                }
+                s += k;
+            }
+        }
+    }
+    __syncthreads();
+    auto start = [&]() -> Walk {
+        Walk w;
+        w.x = entry_of(cta, sh_w, sh_ctas);
+        w.x1 = entry_of(cta + 1, sh_w, sh_ctas);
+        w.u = w.x < w.x1 ? sh_unit : 0;
+        w.ustart = w.x < w.x1 ? sh_first : 0;
+        w.slot = 0;
+        return w;
+    };
+
+    uint8_t *slots = smem + SM::kSlotOff;
+    const int hq = a.hkv * a.g;
+    Piece p;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    }
+
+    if (warp == 0) {  // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = tc::idesc_f16(0, 0, 0, 0, 128, kKeys);
+            constexpr uint32_t idesc_pv = tc::idesc_f16(0, 0, 0, 1, 128, D);
+            uint32_t j = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // operand tiles, P and Q tiles used
+            bool ok = true;
+            auto wait_slot = [&](uint32_t jj) {
+                ok = ok && mbar_wait_bounded(&slot_full[jj % kSlots], (jj / kSlots) & 1);
+                tc::fence_after_sync();
+            };
+            auto qk = [&](int m, uint32_t jj) {
+                const uint32_t qt = smem_u32(smem + m * SM::kTile);
+                const uint32_t kt = smem_u32(slots + (jj % kSlots) * SM::kTile);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks / 4) * SM::kHalf + (ks % 4) * 32;
+                    tc::mma_f16_ss(tmem + m * kKeys, tc::smem_desc(qt + off, 16, 1024),
+                                   tc::smem_desc(kt + off, 16, 1024), idesc_qk, ks > 0 ? 1u : 0u);
+                }
+                tc::commit(&s_full[m]);
+            };
+            for (Walk w = start(); ok && w.next(a, p);) {
+                const int T = p.t1 - p.t0, nm = p.rows > 128 ? 2 : 1;
+                wait_slot(j);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    if (m < nm) {
+                        ok = ok && mbar_wait_bounded(&q_ready[m], nq[m]++ & 1);
+                        tc::fence_after_sync();
+                        if (ok) qk(m, j);
+                    }
+                if (!ok) break;
+                tc::commit(&slot_free[j % kSlots]);
+                for (int i = 0; i < T && ok; ++i) {
+                    const uint32_t jv = j + 1, jk = j + 2;
+                    wait_slot(jv);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        if (m >= nm || !ok) break;
+                        ok = mbar_wait_bounded(&p_full[m], np[m]++ & 1);
+                        tc::fence_after_sync();
+                        if (!ok) break;
+                        const uint32_t vt = smem_u32(slots + (jv % kSlots) * SM::kTile);
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk) {
+                            const uint64_t bd = tc::smem_desc(vt + kk * 16 * 128, SM::kHalf, 1024);
+                            const uint32_t pt = tmem + m * kKeys + (kk / 2) * 32 + (kk % 2) * 8;
+                            tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt, bd, idesc_pv, kk > 0 ? 1u : 0u);
+                            tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt + 16, bd, idesc_pv, 1u);
+                        }
+                        if (m == nm - 1) tc::commit(&slot_free[jv % kSlots]);
+                        if (i + 1 < T) {
+                            if (m == 0) wait_slot(jk);
+                            if (!ok) break;
+                            qk(m, jk);
+                            if (m == nm - 1) tc::commit(&slot_free[jk % kSlots]);
+                        } else {
+                            tc::commit(&s_full[m]);  // the last P V of the piece
+                        }
+                    }
+                    j += 2;
+                }
+            }
+            if (!ok) set_error(a.err, RESA_DEVERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp < 4) {  // ------------------------------------------- converters
+        const int ct = tid - 32;
+        const int bs_shift = a.bs == 64 ? 6 : a.bs == 32 ? 5 : 4;
+        const int bpt = kKeys >> bs_shift;  // blocks a tile
+        uint8_t *raw = smem + SM::kRawOff;
+        const uint32_t raw_s = smem_u32(raw);
+        uint32_t j = 0, tiles = 0;
+        bool ok = true;
+        for (Walk w = start(); w.next(a, p);) {
+            const int T = p.t1 - p.t0;
+            const int nblk = (p.L + a.bs - 1) >> bs_shift;
+            const int32_t *pages = a.page_table + (size_t)p.row * a.max_pages;
+            // Page ids 32 blocks at a time, one a lane, the next window in flight.
+            const int blk0 = p.t0 * bpt, blk1 = min(nblk, p.t1 * bpt);
+            auto load_win = [&](int w32) -> int {
+                const int blk = blk0 + w32 * 32 + lane;
+                return blk < blk1 ? pages[blk] : -1;
+            };
+            int win_cur = load_win(0), win_next = load_win(1), win = 0;
+            uint32_t masks[kRaw];  // valid blocks of the tiles in flight, oldest first
+            // Bring tile t of the piece into raw stage st; returns its valid blocks.
+            auto issue = [&](int t, uint32_t st) -> uint32_t {
+                uint32_t mask = 0;
+                if (t < T) {
+                    const int first = t * bpt;
+                    if (first >> 5 != win) {
+                        win_cur = win_next;
+                        ++win;
+                        win_next = load_win(win + 1);
+                    }
+                    int page = __shfl_sync(0xffffffffu, win_cur, (first + lane) & 31);
+                    const int blk = blk0 + first + lane;
+                    const bool there = lane < bpt && blk < blk1;
+                    if (there && (page < 0 || page >= a.num_pages)) {
+                        set_error(a.err, RESA_DEVERR_PAGE);
+                        page = -1;
+                    }
+                    if (!there) page = -1;
+                    mask = __ballot_sync(0xffffffffu, page >= 0);
+                    const uint32_t base = raw_s + st * SM::kRawStage;
+                    constexpr int kPerRow = D / 32, kChunks = kKeys * kPerRow;
+#pragma unroll 1
+                    for (int k = 0; k < (kChunks + kConv - 1) / kConv; ++k) {
+                        const int e = ct + k * kConv;
+                        const int r = e / kPerRow, c = e % kPerRow;
+                        const int pg = __shfl_sync(0xffffffffu, page, (r >> bs_shift) & 31);
+                        if (e < kChunks && pg >= 0) {
+                            const size_t slot = (((size_t)pg * a.hkv + p.h) << bs_shift) + (r & (a.bs - 1));
+                            const size_t at = slot * (D / 2) + c * 16;
+                            const uint32_t dst = base + raw_chunk<D>(r, c);
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                                         "l"(a.c.k + at) : "memory");
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + SM::kCodes),
+                                         "l"(a.c.v + at) : "memory");
+                        }
+                    }
+                    constexpr int kScRows = 256 / D;  // rows a 16-byte chunk of scales
+                    constexpr int kSc = kKeys / kScRows;
+                    const int r = ct * kScRows;
+                    const int pg = __shfl_sync(0xffffffffu, page, (r >> bs_shift) & 31);
+                    if (ct < kSc && pg >= 0) {
+                        const size_t slot = (((size_t)pg * a.hkv + p.h) << bs_shift) + (r & (a.bs - 1));
+                        const uint32_t dst = base + 2 * SM::kCodes + ct * 16;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                                     "l"(a.c.k_sf + slot * (D / 16)) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + SM::kScales),
+                                     "l"(a.c.v_sf + slot * (D / 16)) : "memory");
+                    }
+                }
+                cp_async_commit();
+                return mask;
+            };
+            conv_sync();  // the last piece's raw tiles are used up
+            masks[0] = issue(0, tiles % kRaw);
+            masks[1] = issue(1, (tiles + 1) % kRaw);
+            for (int t = 0; t < T; ++t, ++tiles) {
+                cp_async_wait<1>();
+                conv_sync();  // tile t is here for everyone, tile t - 1 used up
+                masks[2] = issue(t + 2, (tiles + 2) % kRaw);
+                const uint32_t mask = masks[0];
+                masks[0] = masks[1];
+                masks[1] = masks[2];
+                const uint8_t *st = raw + (tiles % kRaw) * SM::kRawStage;
+                const int left = p.L - (p.t0 + t) * kKeys;  // rows of the tile below the length
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++j) {
+                    if (j >= kSlots)
+                        ok = ok && mbar_wait_bounded(&slot_free[j % kSlots], ((j / kSlots) - 1) & 1);
+                    if (kv == 0 && ct == 0) {
+                        uint32_t m16 = 0;
+                        for (int x = 0; x < kKeys / 16; ++x)
+                            m16 |= ((mask >> ((x * 16) >> bs_shift)) & 1u) << x;
+                        tile_mask[tiles & 3] = m16;
+                    }
+                    uint8_t *dst = slots + (j % kSlots) * SM::kTile;
+                    const uint8_t *codes = st + kv * SM::kCodes;
+                    const uint8_t *scales = st + 2 * SM::kCodes + kv * SM::kScales;
+                    constexpr int kPerRow = D / 32, kChunks = kKeys * kPerRow;
+#pragma unroll 1
+                    for (int k = 0; k < (kChunks + kConv - 1) / kConv; ++k) {
+                        const int e = ct + k * kConv;
+                        if (e >= kChunks) break;
+                        // eight lanes take the same chunk of eight rows: no bank conflicts
+                        const int c = (e / 8) % kPerRow, r = (e % 8) + 8 * (e / (8 * kPerRow));
+                        const uint4 x = *reinterpret_cast<const uint4 *>(codes + raw_chunk<D>(r, c));
+                        uint32_t sf = *reinterpret_cast<const uint16_t *>(scales + r * (D / 16) + c * 2);
+                        if (r >= left || !((mask >> (r >> bs_shift)) & 1u)) sf = 0;  // counts as 0
+                        const uint32_t s2 = e4m3x2_to_f16(sf);
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                        uint8_t *row = dst + (c / 2) * SM::kHalf;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t s = __byte_perm(s2, s2, i < 2 ? 0x1010 : 0x3232);
+                            uint32_t y[4];
+                            e2m1x8_to_f16(xs[i], y);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) y[z] = mul_f16x2(y[z], s);
+                            *reinterpret_cast<uint4 *>(row + swz128(r, (c % 2) * 4 + i)) =
+                                make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&slot_full[j % kSlots]);
+                }
+            }
+            cp_async_wait<0>();
+        }
+        if (!ok && ct == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+    } else {  // ---------------------------------------------------------- softmax
+        const int m = (warp - 4) >> 2, r = (tid - 128) & 127;
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t scol = tmem + lane_base + m * kKeys;
+        const uint32_t ocol = tmem + lane_base + 2 * kKeys + m * D;
+        uint32_t ns = 0, tiles = 0;  // S tiles (and last P V) seen, key tiles so far
+        bool ok = true;
+        for (Walk w = start(); w.next(a, p); tiles += (uint32_t)(p.t1 - p.t0)) {
+            const int T = p.t1 - p.t0, nm = p.rows > 128 ? 2 : 1;
+            const int lrow = m * 128 + r, rho = p.row0 + lrow;
+            const bool row_ok = lrow < p.rows;
+            const int pos_first = p.L - p.n;
+            const int lim = row_ok ? pos_first + rho / a.g + 1 : 0;  // keys the row sees
+            const int lim_warp = pos_first + (rho - lane) / a.g + 1;  // keys every row of the warp sees
+            const size_t orow = ((size_t)p.b * a.f + rho / a.g) * hq + (size_t)p.h * a.g + rho % a.g;
+            // Q row, scaled to [2^8, 2^9) at its largest, into the swizzled tile
+            int e = 0;
+            if (m < nm) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + orow * D);
+                uint32_t mag = 0;
+                if (row_ok) {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 x = src[c];
+                        mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+                    }
+                    mag = max(mag & 0xffffu, mag >> 16);
+                    // zero and non-finite rows keep factor 1
+                    if (mag != 0 && mag < 0x7f80u) e = max(-110, min(119, (int)(mag >> 7) - 127 - 8));
+                }
+                const float f2 = pow2i(-e);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = row_ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 y = make_uint4(pack_f16(bf_lo(x.x) * f2, bf_hi(x.x) * f2),
+                                               pack_f16(bf_lo(x.y) * f2, bf_hi(x.y) * f2),
+                                               pack_f16(bf_lo(x.z) * f2, bf_hi(x.z) * f2),
+                                               pack_f16(bf_lo(x.w) * f2, bf_hi(x.w) * f2));
+                    *reinterpret_cast<uint4 *>(smem + m * SM::kTile + (c / 8) * SM::kHalf +
+                                               swz128(r, c % 8)) = y;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&q_ready[m]);
+            }
+            if (m >= nm) continue;
+            const float rs = a.scale_log2 * head_scale(a.c.k_scale, p.h) * pow2i(e);
+            float mx = -INFINITY, l = 0.f, alpha = 0.f;
+            float acc[D];
+#pragma unroll
+            for (int c = 0; c < D; ++c) acc[c] = 0.f;
+            for (int i = 0; i < T; ++i) {
+                ok = ok && mbar_wait_bounded(&s_full[m], ns & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ++ns;
+                tc::fence_after_sync();
+                const int t0 = (p.t0 + i) * kKeys;
+                const uint32_t tm = tile_mask[(tiles + i) & 3];
+                const bool full = tm == (1u << (kKeys / 16)) - 1u && t0 + kKeys <= lim_warp;
+                if (i > 0) {  // the last tile's O
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t ov[32];
+                        tc::tmem_ld32(ocol + 32 * c, ov);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            acc[32 * c + x] = fmaf(acc[32 * c + x], alpha, __uint_as_float(ov[x]));
+                    }
+                }
+                // the row's largest logit
+                float mt = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    uint32_t sv[32];
+                    tc::tmem_ld32(scol + 32 * c, sv);
+                    tc::tmem_wait_ld();
+                    if (full) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) mt = fmaxf(mt, __uint_as_float(sv[x]));
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            const int k = 32 * c + x;
+                            if (t0 + k < lim && ((tm >> (k / 16)) & 1u)) mt = fmaxf(mt, __uint_as_float(sv[x]));
+                        }
+                    }
+                }
+                mt *= rs;
+                // a whole number, so that every factor 2^(m - m') is exact
+                const float mn = mt > mx ? ceilf(mt) : mx;
+                const float al = mx == -INFINITY ? 0.f : ex2(mx - mn);
+                mx = mn;
+                const float nb = mn == -INFINITY ? 0.f : kShift - mn;
+                float ls[2] = {0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    uint32_t sv[32];
+                    tc::tmem_ld32(scol + 32 * c, sv);
+                    tc::tmem_wait_ld();
+                    if (!full) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            const int k = 32 * c + x;
+                            if (!(t0 + k < lim && ((tm >> (k / 16)) & 1u))) sv[x] = 0xff800000u;
+                        }
+                    }
+                    uint32_t pw[32];  // 16 columns of hi, 16 of lo
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const float p0 = ex2(fmaf(__uint_as_float(sv[2 * x]), rs, nb));
+                        const float p1 = ex2(fmaf(__uint_as_float(sv[2 * x + 1]), rs, nb));
+                        ls[0] += p0;
+                        ls[1] += p1;
+                        pw[x] = pack_f16(p0, p1);
+                        pw[16 + x] = pack_f16(p0 - f16_lo(pw[x]), p1 - f16_hi(pw[x]));
+                    }
+                    tc::tmem_st32(scol + 32 * c, pw);
+                }
+                l = fmaf(l, al, ls[0] + ls[1]);
+                alpha = al;
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(&p_full[m]);
+            }
+            ok = ok && mbar_wait_bounded(&s_full[m], ns & 1);  // the last P V
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ++ns;
+            tc::fence_after_sync();
+            const bool whole = p.t0 == 0 && p.t1 == p.cnt;
+            const float inv = l > 0.f ? head_scale(a.c.v_scale, p.h) / l : (l == 0.f ? 0.f : l);
+            const size_t slot = (size_t)(2 * cta + p.slot) * kRows + lrow;
+            float *dst = whole ? a.out + orow * D : a.part_o + slot * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                tc::tmem_ld32(ocol + 32 * c, ov);
+                tc::tmem_wait_ld();
+                if (row_ok) {
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        float4 v;
+                        v.x = fmaf(acc[32 * c + x], alpha, __uint_as_float(ov[x]));
+                        v.y = fmaf(acc[32 * c + x + 1], alpha, __uint_as_float(ov[x + 1]));
+                        v.z = fmaf(acc[32 * c + x + 2], alpha, __uint_as_float(ov[x + 2]));
+                        v.w = fmaf(acc[32 * c + x + 3], alpha, __uint_as_float(ov[x + 3]));
+                        if (whole) {
+                            v.x *= inv;
+                            v.y *= inv;
+                            v.z *= inv;
+                            v.w *= inv;
+                        }
+                        *reinterpret_cast<float4 *>(dst + 32 * c + x) = v;
+                    }
+                }
+            }
+            if (row_ok) {
+                if (!whole)
+                    a.part_ml[slot] = make_float2(mx, l);
+                else if (a.lse)
+                    a.lse[orow] = l > 0.f ? (mx - kShift + log2f(l)) * 0.6931471805599453f
+                                  : l == 0.f ? -INFINITY : l;
+            }
+            tc::fence_before_sync();
+        }
+        if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+    }
+    // the launch's share again for what follows
+    __syncwarp();
+    if (warp < 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 168;");
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+
+    // The errors of every sequence.
+    for (int u = cta * kThreads + tid; u < units; u += gridDim.x * kThreads) chunk_unit(a, u, a.err);
+    if (gridDim.x == 1) return;
+
+    // Merge the units that span CTAs: their CTAs take an equal share of the rows.
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) sh_ok = grid_barrier_bounded(a.grid_bar, gridDim.x) ? 1u : 0u;
+    __syncthreads();
+    if (!sh_ok) {
+        if (tid == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+        return;
+    }
+    __threadfence();
+    for (Walk w = start(); w.next(a, p);) {
+        if (p.t0 == 0 && p.t1 == p.cnt) continue;
+        const int W = sh_w, G = sh_ctas;
+        const int q0 = (int)((((long long)p.ustart + 1) * G - 1) / W);
+        const int q1 = (int)((((long long)p.ustart + p.cnt) * G - 1) / W);
+        const int k = q1 - q0 + 1, mine_i = cta - q0;
+        const int r0 = (int)((long long)p.rows * mine_i / k), r1 = (int)((long long)p.rows * (mine_i + 1) / k);
+        const float vg = head_scale(a.c.v_scale, p.h);
+        for (int lrow = r0 + warp; lrow < r1; lrow += kThreads / 32) {
+            auto slot_of = [&](int q) -> size_t {
+                return (size_t)(2 * q + (entry_of(q, W, G) >= p.ustart ? 0 : 1)) * kRows + lrow;
+            };
+            float ms = -INFINITY;
+            for (int q = q0 + lane; q <= q1; q += 32) ms = fmaxf(ms, __ldcg(&a.part_ml[slot_of(q)]).x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o));
+            constexpr int kV = D / 32;  // channels a lane
+            float ls = 0.f, os[kV];
+#pragma unroll
+            for (int x = 0; x < kV; ++x) os[x] = 0.f;
+#pragma unroll 4
+            for (int q = q0; q <= q1; ++q) {
+                const size_t sl = slot_of(q);
+                const float2 ml = __ldcg(&a.part_ml[sl]);
+                const float f2 = ms == -INFINITY ? 0.f : ex2(ml.x - ms);
+                ls += ml.y * f2;
+                const float *src = a.part_o + sl * D + lane * kV;
+                if constexpr (kV == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    os[0] += v.x * f2;
+                    os[1] += v.y * f2;
+                    os[kV - 2] += v.z * f2;
+                    os[kV - 1] += v.w * f2;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    os[0] += v.x * f2;
+                    os[1] += v.y * f2;
+                }
+            }
+            const int rho = p.row0 + lrow;
+            const size_t orow = ((size_t)p.b * a.f + rho / a.g) * hq + (size_t)p.h * a.g + rho % a.g;
+            const float inv = ls > 0.f ? vg / ls : (ls == 0.f ? 0.f : ls);
+#pragma unroll
+            for (int x = 0; x < kV; ++x) a.out[orow * D + lane * kV + x] = os[x] * inv;
+            if (a.lse && lane == 0)
+                a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * 0.6931471805599453f
+                              : ls == 0.f ? -INFINITY : ls;
+        }
+    }
+}
+
+template <int D>
+cudaError_t launch_t(const ChunkArgs &a, int ctas, cudaStream_t st) {
+    constexpr int smem = ChunkSmem<D>::kBytes;
+    static std::atomic<int> done[64];
+    cudaError_t e = ensure_smem(chunk_q4_kernel<D>, smem, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, chunk_q4_kernel<D>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
+                            const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
+                            int sms, float *part_o, float *part_ml, uint32_t *grid_bar, float *out,
+                            float *lse, uint32_t *err, cudaStream_t st) {
+    ChunkArgs a{};
+    a.c = c;
+    a.page_table = page_table;
+    a.seq_len = seq_len;
+    a.n_new = n_new;
+    a.q = static_cast<const uint16_t *>(q);
+    a.part_o = part_o;
+    a.out = out;
+    a.lse = lse;
+    a.part_ml = reinterpret_cast<float2 *>(part_ml);
+    a.grid_bar = reinterpret_cast<unsigned long long *>(grid_bar);
+    a.err = err;
+    a.rm = s.rows;
+    a.f = f;
+    a.batch = s.batch;
+    a.hkv = s.hkv;
+    a.g = s.g;
+    a.groups = rect_row_groups(f, s.g);
+    a.max_pages = s.max_pages;
+    a.num_pages = s.num_pages;
+    a.bs = s.bs;
+    a.scale_log2 = s.sm_scale * 1.4426950408889634f;
+    // one CTA per SM, no more than the longest sequences could use
+    const long long most = (long long)s.batch * s.hkv * a.groups *
+                           (((long long)s.max_pages * s.bs + kKeys - 1) / kKeys);
+    long long ctas = sms < kNumSms ? sms : kNumSms;
+    const long long need = (most + kMinTiles - 1) / kMinTiles;
+    if (need < ctas) ctas = need;
+    return s.d == 128 ? launch_t<128>(a, (int)ctas, st) : launch_t<64>(a, (int)ctas, st);
+}
+
+}  // namespace resa

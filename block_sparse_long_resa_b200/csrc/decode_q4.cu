@@ -124,7 +124,7 @@ struct DecodeQ4Args {
     float2 *part_ml;
     uint32_t *tickets, *err;
     RowMap rm;
-    int f, row0, max_topk, batch, hq, hkv, g, max_pages, num_pages, bs;
+    int f, max_topk, batch, hq, hkv, g, max_pages, num_pages, bs;
     float scale_log2;
 };
 
@@ -173,14 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.live = false;
                 return x;
             }
-            // rows row0 .. row0 + 15 of the chunk see positions below lim
-            const int rows = min(x.n * a.g - a.row0, kMaxGroup);
-            if (rows <= 0) {
-                x.live = false;
-                return x;
-            }
-            const int lim = x.L - x.n + (a.row0 + rows - 1) / a.g + 1;
-            x.cnt = (lim + a.bs - 1) / a.bs;
+            x.cnt = (x.L + a.bs - 1) / a.bs;
         } else {
             x.cnt = max(0, min(a.block_cnt[u], a.max_topk + 1));
         }
@@ -236,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long uend = ustart + un.cnt;
         const int j0 = (int)(x - ustart), j1 = (int)(min(x1, uend) - ustart);  // entries of this piece
         const int b = un.b, h = un.h, L = un.L;
-        const int rows_all = a.block_idx ? a.g : min(un.n * a.g - a.row0, kMaxGroup);
+        const int rows_all = a.block_idx ? a.g : un.n * a.g;
         const int base_pos = a.block_idx ? 0 : L - un.n;  // row rho sees positions <= base_pos + rho / g
         const int nblk_seq = (L + a.bs - 1) / a.bs;
         const int32_t *list =
@@ -328,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < NT; ++n) {
             const int rho = n * 8 + r;
             const bool ok = rho < rows_all;
-            const int qr = a.row0 + (ok ? rho : 0);
+            const int qr = ok ? rho : 0;
             const size_t qrow = ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow * D + c * (D / 4));
             uint4 x[D / 32];
@@ -362,10 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 row_scale[n][k] = __shfl_sync(0xffffffffu, sc, (2 * c + k) * 4);
                 lim[n][k] = row >= rows_all ? 0
                             : a.block_idx   ? L
-                                            : base_pos + (a.row0 + row) / a.g + 1;
+                                            : base_pos + row / a.g + 1;
             }
         }
-        const int lim_all = a.block_idx ? L : base_pos + a.row0 / a.g + 1;  // every row sees these
+        const int lim_all = a.block_idx ? L : base_pos + 1;  // every row sees these
 
         float m[NT][2], l[NT][2], o[D / 16][NT][4];
 #pragma unroll
@@ -585,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float vg = head_scale(a.c.v_scale, h);
         const float kLn2 = 0.6931471805599453f;
         auto orow_of = [&](int rho) -> size_t {
-            const int qr = a.row0 + rho;
+            const int qr = rho;
             return ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
         };
         // partial slot of CTA q for this unit: 2q when its share starts in the
@@ -679,7 +672,7 @@ cudaError_t launch_t(const DecodeQ4Args &a, int ctas, cudaStream_t st) {
 
 cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
                              const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
-                             int row0, const int32_t *block_idx, const int32_t *block_cnt,
+                             const int32_t *block_idx, const int32_t *block_cnt,
                              int max_topk, int sms, float *part_o, float *part_ml,
                              uint32_t *tickets, float *out, float *lse, uint32_t *err,
                              cudaStream_t st) {
@@ -699,7 +692,6 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     a.err = err;
     a.rm = s.rows;
     a.f = f;
-    a.row0 = row0;
     a.max_topk = max_topk;
     a.batch = s.batch;
     a.hq = s.hq;
@@ -711,7 +703,7 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     a.scale_log2 = s.sm_scale * 1.4426950408889634f;
     // one CTA per SM; two partial slots a CTA in the decode partials
     const int ctas = sms < kNumSms ? sms : kNumSms;
-    const int rows = block_idx ? s.g : (f * s.g - row0 < kMaxGroup ? f * s.g - row0 : kMaxGroup);
+    const int rows = block_idx ? s.g : f * s.g;
     if (s.d == 128) return rows <= 8 ? launch_t<128, 1>(a, ctas, st) : launch_t<128, 2>(a, ctas, st);
     return rows <= 8 ? launch_t<64, 1>(a, ctas, st) : launch_t<64, 2>(a, ctas, st);
 }

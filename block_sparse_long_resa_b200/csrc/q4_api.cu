@@ -149,7 +149,7 @@ resa_status_t resa_sparse_decode_q4(const resa_config_t *cfg, const resa_cache_q
         return RESA_ERR_UNSUPPORTED;
     const WsLayout w = layout_of(s, 0);
     RESA_TRY(check_ws(ws, ws_bytes, w));
-    return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, 1, nullptr, 0,
+    return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, 1, nullptr,
                                         block_idx, block_cnt, max_topk, sm_count(),
                                         at<float>(ws, w.dec_o), at<float>(ws, w.dec_lse),
                                         at<uint32_t>(ws, w.dec_ticket), out, lse_opt,
@@ -169,14 +169,20 @@ resa_status_t resa_attention_q4(const resa_config_t *cfg, const resa_cache_q4_t 
     if (rect_row_groups(f, s.g) > kMaxRowTiles) return RESA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || !aligned4(n_new_opt) || !aligned4(lse_opt))
         return RESA_ERR_UNSUPPORTED;
-    const WsLayout w = layout_of(s, f == 1 ? 0 : f);
+    const WsLayout w = layout_of(s, f * s.g <= kMaxGroup ? 0 : f);
     RESA_TRY(check_ws(ws, ws_bytes, w));
-    for (int row0 = 0; row0 < f * s.g; row0 += kMaxGroup)
-        RESA_TRY(cuda_status(launch_decode_q4(
-            s, c, cache->page_table, cache->seq_len, q, f, n_new_opt, row0, nullptr, nullptr, 0,
-            sm_count(), at<float>(ws, w.dec_o), at<float>(ws, w.dec_lse),
-            at<uint32_t>(ws, w.dec_ticket), out, lse_opt, at<uint32_t>(ws, w.err), stream)));
-    return RESA_OK;
+    if ((long long)s.batch * s.hkv * rect_row_groups(f, s.g) * (((long long)s.max_pages * s.bs + 127) / 128) >
+        0x7fffffffLL)
+        return RESA_ERR_RANGE;
+    uint32_t *err = at<uint32_t>(ws, w.err);
+    if (f * s.g <= kMaxGroup)
+        return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
+                                            nullptr, nullptr, 0, sm_count(), at<float>(ws, w.dec_o),
+                                            at<float>(ws, w.dec_lse), at<uint32_t>(ws, w.dec_ticket),
+                                            out, lse_opt, err, stream));
+    return cuda_status(launch_chunk_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
+                                       sm_count(), at<float>(ws, w.rect_o), at<float>(ws, w.rect_lse),
+                                       at<uint32_t>(ws, w.rect_ticket), out, lse_opt, err, stream));
 }
 
 }  // extern "C"

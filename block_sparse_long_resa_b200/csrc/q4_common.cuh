@@ -126,12 +126,18 @@ cudaError_t launch_expand_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
                              cudaStream_t st);
 // Split-KV attention over a 4-bit cache.  block_idx == nullptr: every position
 // (query rows f, row r of n sees positions 0 .. L - n + r); else the listed
-// blocks (f = 1).  At most kMaxGroup rows f * g from row row0 on.
+// blocks (f = 1).  At most kMaxGroup rows f * g.
 cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
                              const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
-                             int row0, const int32_t *block_idx, const int32_t *block_cnt,
+                             const int32_t *block_idx, const int32_t *block_cnt,
                              int max_topk, int sms, float *part_o, float *part_ml,
                              uint32_t *tickets, float *out, float *lse, uint32_t *err,
                              cudaStream_t st);
+// The same for chunks of more than kMaxGroup rows, on tcgen05 (part_o and part_ml: two row
+// groups a CTA; grid_bar: a 64-bit barrier word).
+cudaError_t launch_chunk_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
+                            const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
+                            int sms, float *part_o, float *part_ml, uint32_t *grid_bar, float *out,
+                            float *lse, uint32_t *err, cudaStream_t st);
 
 }  // namespace resa
