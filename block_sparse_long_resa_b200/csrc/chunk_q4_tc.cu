@@ -60,20 +60,38 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 operations at a time.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ void conv_sync() { asm volatile("bar.sync 1, 96;" ::: "memory"); }
 
-// Byte offset of 16-byte chunk c of row r of a raw code tile: within a 128-byte
-// line the chunks are XORed so that eight consecutive rows' chunks c meet all banks.
-template <int D>
-__device__ __forceinline__ uint32_t raw_chunk(int r, int c) {
-    constexpr int kPerRow = D / 32, kRowsPerLine = 8 / kPerRow;
-    const int line = r / kRowsPerLine;
-    return (uint32_t)(line * 128 + ((r % kRowsPerLine) * kPerRow + (c ^ (line & (kPerRow - 1)))) * 16);
+__device__ __forceinline__ void cp_async16_s(uint32_t smem_dst, const void *gsrc) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
 }
 
 struct ChunkArgs {
@@ -172,9 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
-    __shared__ uint64_t q_ready[2], slot_full[kSlots], slot_free[kSlots], s_full[2], p_full[2];
+    __shared__ uint64_t q_ready[2], slot_full[kSlots], slot_free[kSlots], s_full[2], o_full[2], p_full[2][2];
     __shared__ uint32_t tmem_base_s, sh_ok;
-    __shared__ uint32_t tile_mask[4];  // valid 16-key blocks of a tile
+    __shared__ uint64_t raw_full[kRaw], raw_free[kRaw];
+    __shared__ uint32_t tile_mask[4];    // a tile's valid runs of 16 keys
     __shared__ int sh_sum[kThreads / 32], sh_w, sh_ctas, sh_first, sh_unit;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -194,6 +213,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) sh_sum[warp] = incl;
     if (tid == 0) {
+        for (int s = 0; s < kRaw; ++s) {
+            mbar_init(&raw_full[s], kConv);
+            mbar_init(&raw_free[s], 3);
+        }
         for (int s = 0; s < kSlots; ++s) {
             mbar_init(&slot_full[s], kConv);
             mbar_init(&slot_free[s], 1);
@@ -201,7 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = 0; m < 2; ++m) {
             mbar_init(&q_ready[m], 128);
             mbar_init(&s_full[m], 1);
-            mbar_init(&p_full[m], 128);
+            mbar_init(&o_full[m], 1);
+            mbar_init(&p_full[m][0], 128);
+            mbar_init(&p_full[m][1], 128);
         }
         fence_mbar_init();
     }
@@ -257,77 +282,108 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     if (warp == 0) {  // ------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = tc::idesc_f16(0, 0, 0, 0, 128, kKeys);
-            constexpr uint32_t idesc_pv = tc::idesc_f16(0, 0, 0, 1, 128, D);
-            uint32_t j = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // operand tiles, P and Q tiles used
-            bool ok = true;
-            auto wait_slot = [&](uint32_t jj) {
-                ok = ok && mbar_wait_bounded(&slot_full[jj % kSlots], (jj / kSlots) & 1);
-                tc::fence_after_sync();
-            };
-            auto qk = [&](int m, uint32_t jj) {
-                const uint32_t qt = smem_u32(smem + m * SM::kTile);
-                const uint32_t kt = smem_u32(slots + (jj % kSlots) * SM::kTile);
+        // The whole warp runs the loop and one elected thread issues: with the
+        // addresses uniform over the warp an MMA issues in its 64 cycles, from
+        // a branch of one thread it took 120.
+        constexpr uint32_t idesc_qk = tc::idesc_f16(0, 0, 0, 0, 128, kKeys / 2);
+        constexpr uint32_t idesc_pv = tc::idesc_f16(0, 0, 0, 1, 128, D);
+        const bool el = tc::elect_one();
+        uint32_t j = 0, np[2] = {0, 0}, nq[2] = {0, 0};  // operand tiles, P and Q tiles used
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(bar, parity));
+            tc::fence_after_sync();
+        };
+        auto wait_slot = [&](uint32_t jj) { wait(&slot_full[jj % kSlots], (jj / kSlots) & 1); };
+        // S of M tile m for keys 64 hf .. of operand tile jj
+        auto qk = [&](int m, uint32_t jj, int hf) {
+            const uint32_t qt = smem_u32(smem + m * SM::kTile);
+            const uint32_t kt = smem_u32(slots + (jj % kSlots) * SM::kTile) + hf * (SM::kHalf / 2);
+            if (el) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint32_t off = (ks / 4) * SM::kHalf + (ks % 4) * 32;
-                    tc::mma_f16_ss(tmem + m * kKeys, tc::smem_desc(qt + off, 16, 1024),
+                    tc::mma_f16_ss(tmem + m * kKeys + hf * 64, tc::smem_desc(qt + off, 16, 1024),
                                    tc::smem_desc(kt + off, 16, 1024), idesc_qk, ks > 0 ? 1u : 0u);
                 }
-                tc::commit(&s_full[m]);
-            };
-            for (Walk w = start(); ok && w.next(a, p);) {
-                const int T = p.t1 - p.t0, nm = p.rows > 128 ? 2 : 1;
-                wait_slot(j);
+            }
+        };
+        // O of M tile m from the P and V of keys 64 hf ..
+        auto pv = [&](int m, uint32_t jj, int hf) {
+            const uint32_t vt = smem_u32(slots + (jj % kSlots) * SM::kTile) + hf * (SM::kHalf / 2);
+            if (el) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                    if (m < nm) {
-                        ok = ok && mbar_wait_bounded(&q_ready[m], nq[m]++ & 1);
-                        tc::fence_after_sync();
-                        if (ok) qk(m, j);
-                    }
-                if (!ok) break;
-                tc::commit(&slot_free[j % kSlots]);
-                for (int i = 0; i < T && ok; ++i) {
-                    const uint32_t jv = j + 1, jk = j + 2;
-                    wait_slot(jv);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        if (m >= nm || !ok) break;
-                        ok = mbar_wait_bounded(&p_full[m], np[m]++ & 1);
-                        tc::fence_after_sync();
-                        if (!ok) break;
-                        const uint32_t vt = smem_u32(slots + (jv % kSlots) * SM::kTile);
-#pragma unroll
-                        for (int kk = 0; kk < kKeys / 16; ++kk) {
-                            const uint64_t bd = tc::smem_desc(vt + kk * 16 * 128, SM::kHalf, 1024);
-                            const uint32_t pt = tmem + m * kKeys + (kk / 2) * 32 + (kk % 2) * 8;
-                            tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt, bd, idesc_pv, kk > 0 ? 1u : 0u);
-                            tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt + 16, bd, idesc_pv, 1u);
-                        }
-                        if (m == nm - 1) tc::commit(&slot_free[jv % kSlots]);
-                        if (i + 1 < T) {
-                            if (m == 0) wait_slot(jk);
-                            if (!ok) break;
-                            qk(m, jk);
-                            if (m == nm - 1) tc::commit(&slot_free[jk % kSlots]);
-                        } else {
-                            tc::commit(&s_full[m]);  // the last P V of the piece
-                        }
-                    }
-                    j += 2;
+                for (int kk = 0; kk < 4; ++kk) {
+                    const uint64_t bd = tc::smem_desc(vt + kk * 16 * 128, SM::kHalf, 1024);
+                    const uint32_t pt = tmem + m * kKeys + hf * 64 + kk * 16;
+                    tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt, bd, idesc_pv, hf > 0 || kk > 0 ? 1u : 0u);
+                    tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt + 8, bd, idesc_pv, 1u);
                 }
             }
-            if (!ok) set_error(a.err, RESA_DEVERR_TIMEOUT);
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (el) tc::commit(bar);
+        };
+        for (Walk w = start(); ok && w.next(a, p);) {
+            const int T = p.t1 - p.t0, nm = p.rows > 128 ? 2 : 1;
+            wait_slot(j);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                if (m < nm) {
+                    wait(&q_ready[m], nq[m]++ & 1);
+                    if (!ok) break;
+                    qk(m, j, 0);
+                    qk(m, j, 1);
+                    commit(&s_full[m]);
+                }
+            if (!ok) break;
+            commit(&slot_free[j % kSlots]);
+            for (int i = 0; i < T && ok; ++i, j += 2) {
+                const uint32_t jv = j + 1, jk = j + 2;
+                const bool more = i + 1 < T;
+                wait_slot(jv);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    if (m >= nm || !ok) break;
+                    // half a tile at a time: the next S of these keys goes over their P
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        wait(&p_full[m][hf], np[m] & 1);
+                        if (!ok) break;
+                        pv(m, jv, hf);
+                        if (hf == 1) commit(&o_full[m]);
+                        if (hf == 1 && m == nm - 1) commit(&slot_free[jv % kSlots]);
+                        if (more) {
+                            if (hf == 0 && m == 0) wait_slot(jk);
+                            if (!ok) break;
+                            qk(m, jk, hf);
+                        }
+                    }
+                    if (!ok) break;
+                    ++np[m];
+                    if (more) {
+                        commit(&s_full[m]);
+                        if (m == nm - 1) commit(&slot_free[jk % kSlots]);
+                    }
+                }
+            }
         }
+        if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
         __syncwarp();
     } else if (warp < 4) {  // ------------------------------------------- converters
-        const int ct = tid - 32;
+        // The 4-bit tiles come in two tiles ahead, by runs of 16 keys (contiguous in the
+        // cache): warp w takes runs w - 1, w + 2, .., a lane 16 bytes at a time.  (Bulk
+        // copies, one a run and array, took 80 cycles each to issue.)
         const int bs_shift = a.bs == 64 ? 6 : a.bs == 32 ? 5 : 4;
         const int bpt = kKeys >> bs_shift;  // blocks a tile
-        uint8_t *raw = smem + SM::kRawOff;
-        const uint32_t raw_s = smem_u32(raw);
+        const uint32_t raw_s = smem_u32(smem + SM::kRawOff), slots_s = smem_u32(slots);
+        // A lane converts the 16-byte chunk c (32 channels) of row r1 of every step of
+        // 32 chunks.  Lanes of the upper channel half take their words in the order
+        // 2 3 0 1, so that the eight lanes of a store phase meet all banks.
+        constexpr int kPerRow = D / 32, kStepRows = 32 / kPerRow;
+        const int r1 = lane / kPerRow, c = lane % kPerRow;
+        const bool swap = c >= 2;
+        const uint32_t x0 = (uint32_t)((((c & 1) * 4) ^ (swap ? 2 : 0) ^ (r1 & 7)) << 4);
         uint32_t j = 0, tiles = 0;
         bool ok = true;
         for (Walk w = start(); w.next(a, p);) {
@@ -341,121 +397,133 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return blk < blk1 ? pages[blk] : -1;
             };
             int win_cur = load_win(0), win_next = load_win(1), win = 0;
-            uint32_t masks[kRaw];  // valid blocks of the tiles in flight, oldest first
-            // Bring tile t of the piece into raw stage st; returns its valid blocks.
-            auto issue = [&](int t, uint32_t st) -> uint32_t {
-                uint32_t mask = 0;
-                if (t < T) {
-                    const int first = t * bpt;
-                    if (first >> 5 != win) {
-                        win_cur = win_next;
-                        ++win;
-                        win_next = load_win(win + 1);
-                    }
-                    int page = __shfl_sync(0xffffffffu, win_cur, (first + lane) & 31);
-                    const int blk = blk0 + first + lane;
-                    const bool there = lane < bpt && blk < blk1;
-                    if (there && (page < 0 || page >= a.num_pages)) {
-                        set_error(a.err, RESA_DEVERR_PAGE);
-                        page = -1;
-                    }
-                    if (!there) page = -1;
-                    mask = __ballot_sync(0xffffffffu, page >= 0);
-                    const uint32_t base = raw_s + st * SM::kRawStage;
-                    constexpr int kPerRow = D / 32, kChunks = kKeys * kPerRow;
-#pragma unroll 1
-                    for (int k = 0; k < (kChunks + kConv - 1) / kConv; ++k) {
-                        const int e = ct + k * kConv;
-                        const int r = e / kPerRow, c = e % kPerRow;
-                        const int pg = __shfl_sync(0xffffffffu, page, (r >> bs_shift) & 31);
-                        if (e < kChunks && pg >= 0) {
-                            const size_t slot = (((size_t)pg * a.hkv + p.h) << bs_shift) + (r & (a.bs - 1));
-                            const size_t at = slot * (D / 2) + c * 16;
-                            const uint32_t dst = base + raw_chunk<D>(r, c);
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                                         "l"(a.c.k + at) : "memory");
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + SM::kCodes),
-                                         "l"(a.c.v + at) : "memory");
+            auto issue = [&](int t) -> uint32_t {  // tile t of the piece; its valid blocks
+                const uint32_t at = tiles + (uint32_t)t, st = at % kRaw;
+                if (at >= kRaw) ok = ok && mbar_wait_bounded(&raw_free[st], ((at / kRaw) - 1) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return 0u;
+                const int first = t * bpt;
+                if (first >> 5 != win) {
+                    win_cur = win_next;
+                    ++win;
+                    win_next = load_win(win + 1);
+                }
+                int page = __shfl_sync(0xffffffffu, win_cur, (first + lane) & 31);
+                const bool there = lane < bpt && blk0 + first + lane < blk1;
+                if (there && (page < 0 || page >= a.num_pages)) {
+                    set_error(a.err, RESA_DEVERR_PAGE);
+                    page = -1;
+                }
+                if (!there) page = -1;
+                const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
+                constexpr int kRunCodes = 16 * D / 2, kRunScales = 16 * D / 16;
+                const uint32_t base = raw_s + st * SM::kRawStage + lane * 16;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const int run = warp - 1 + 3 * k;
+                    const int pg = __shfl_sync(0xffffffffu, page, (run << 4) >> bs_shift);
+                    if (run < kKeys / 16 && pg >= 0) {
+                        const size_t at16 = ((((size_t)pg * a.hkv + p.h) << bs_shift) >> 4) +
+                                            (run & ((a.bs >> 4) - 1));  // run of 16 keys in the cache
+                        const uint8_t *gk = a.c.k + at16 * kRunCodes + lane * 16;
+                        const uint8_t *gv = a.c.v + at16 * kRunCodes + lane * 16;
+                        const uint32_t dst = base + run * kRunCodes;
+#pragma unroll
+                        for (int x = 0; x < kRunCodes; x += 512) {
+                            cp_async16_s(dst + x, gk + x);
+                            cp_async16_s(dst + SM::kCodes + x, gv + x);
+                        }
+                        constexpr int kSc = kRunScales / 16;  // chunks of scales
+                        if (lane < 2 * kSc) {
+                            const bool is_v = lane >= kSc;
+                            cp_async16_s(base + 2 * SM::kCodes + run * kRunScales +
+                                             (is_v ? SM::kScales - kRunScales : 0),
+                                         (is_v ? a.c.v_sf - kRunScales : a.c.k_sf) + at16 * kRunScales + lane * 16);
                         }
                     }
-                    constexpr int kScRows = 256 / D;  // rows a 16-byte chunk of scales
-                    constexpr int kSc = kKeys / kScRows;
-                    const int r = ct * kScRows;
-                    const int pg = __shfl_sync(0xffffffffu, page, (r >> bs_shift) & 31);
-                    if (ct < kSc && pg >= 0) {
-                        const size_t slot = (((size_t)pg * a.hkv + p.h) << bs_shift) + (r & (a.bs - 1));
-                        const uint32_t dst = base + 2 * SM::kCodes + ct * 16;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                                     "l"(a.c.k_sf + slot * (D / 16)) : "memory");
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + SM::kScales),
-                                     "l"(a.c.v_sf + slot * (D / 16)) : "memory");
-                    }
                 }
-                cp_async_commit();
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&raw_full[st]))
+                             : "memory");
                 return mask;
             };
-            conv_sync();  // the last piece's raw tiles are used up
-            masks[0] = issue(0, tiles % kRaw);
-            masks[1] = issue(1, (tiles + 1) % kRaw);
-            for (int t = 0; t < T; ++t, ++tiles) {
-                cp_async_wait<1>();
-                conv_sync();  // tile t is here for everyone, tile t - 1 used up
-                masks[2] = issue(t + 2, (tiles + 2) % kRaw);
+            uint32_t masks[3];  // of this tile and the next two
+            masks[0] = issue(0);
+            masks[1] = T > 1 ? issue(1) : 0u;
+            for (int t = 0; t < T; ++t) {
+                masks[2] = t + 2 < T ? issue(t + 2) : 0u;
+                const uint32_t at = tiles + (uint32_t)t, st = at % kRaw;
+                ok = ok && mbar_wait_bounded(&raw_full[st], (at / kRaw) & 1);
                 const uint32_t mask = masks[0];
                 masks[0] = masks[1];
                 masks[1] = masks[2];
-                const uint8_t *st = raw + (tiles % kRaw) * SM::kRawStage;
                 const int left = p.L - (p.t0 + t) * kKeys;  // rows of the tile below the length
+                const bool whole_tile = left >= kKeys && mask == (1u << bpt) - 1u;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++j) {
                     if (j >= kSlots)
                         ok = ok && mbar_wait_bounded(&slot_free[j % kSlots], ((j / kSlots) - 1) & 1);
-                    if (kv == 0 && ct == 0) {
+                    if (kv == 0 && tid == 32) {
                         uint32_t m16 = 0;
                         for (int x = 0; x < kKeys / 16; ++x)
                             m16 |= ((mask >> ((x * 16) >> bs_shift)) & 1u) << x;
-                        tile_mask[tiles & 3] = m16;
+                        tile_mask[at & 3] = m16;
                     }
-                    uint8_t *dst = slots + (j % kSlots) * SM::kTile;
-                    const uint8_t *codes = st + kv * SM::kCodes;
-                    const uint8_t *scales = st + 2 * SM::kCodes + kv * SM::kScales;
-                    constexpr int kPerRow = D / 32, kChunks = kKeys * kPerRow;
-#pragma unroll 1
-                    for (int k = 0; k < (kChunks + kConv - 1) / kConv; ++k) {
-                        const int e = ct + k * kConv;
-                        if (e >= kChunks) break;
-                        // eight lanes take the same chunk of eight rows: no bank conflicts
-                        const int c = (e / 8) % kPerRow, r = (e % 8) + 8 * (e / (8 * kPerRow));
-                        const uint4 x = *reinterpret_cast<const uint4 *>(codes + raw_chunk<D>(r, c));
-                        uint32_t sf = *reinterpret_cast<const uint16_t *>(scales + r * (D / 16) + c * 2);
-                        if (r >= left || !((mask >> (r >> bs_shift)) & 1u)) sf = 0;  // counts as 0
-                        const uint32_t s2 = e4m3x2_to_f16(sf);
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                        uint8_t *row = dst + (c / 2) * SM::kHalf;
+                    const uint32_t code_at = raw_s + st * SM::kRawStage + kv * SM::kCodes + lane * 16;
+                    const uint32_t scale_at = raw_s + st * SM::kRawStage + 2 * SM::kCodes + kv * SM::kScales +
+                                              lane * 2;
+                    const uint32_t dst = slots_s + (j % kSlots) * SM::kTile + (c / 2) * SM::kHalf + r1 * 128 + x0;
+                    constexpr int kSteps = (kKeys / kStepRows + 2) / 3;
+                    uint32_t xs[kSteps][4];
+                    uint16_t sf[kSteps];
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const int step = warp - 1 + 3 * k;
+                        if (step < kKeys / kStepRows) {
+                            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(xs[k][0]), "=r"(xs[k][1]), "=r"(xs[k][2]), "=r"(xs[k][3])
+                                         : "r"(code_at + step * 512));
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sf[k]) : "r"(scale_at + step * 64));
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        const int step = warp - 1 + 3 * k;
+                        if (step >= kKeys / kStepRows) break;
+                        if (!whole_tile) {
+                            const int r = step * kStepRows + r1;
+                            if (r >= left || !((mask >> (r >> bs_shift)) & 1u)) sf[k] = 0;  // counts as 0
+                        }
+                        const uint32_t s2 = e4m3x2_to_f16(sf[k]);
+                        const uint32_t sw[2] = {__byte_perm(s2, s2, swap ? 0x3232 : 0x1010),
+                                                __byte_perm(s2, s2, swap ? 0x1010 : 0x3232)};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint32_t s = __byte_perm(s2, s2, i < 2 ? 0x1010 : 0x3232);
                             uint32_t y[4];
-                            e2m1x8_to_f16(xs[i], y);
+                            e2m1x8_to_f16(swap ? xs[k][i ^ 2] : xs[k][i], y);
 #pragma unroll
-                            for (int z = 0; z < 4; ++z) y[z] = mul_f16x2(y[z], s);
-                            *reinterpret_cast<uint4 *>(row + swz128(r, (c % 2) * 4 + i)) =
-                                make_uint4(y[0], y[1], y[2], y[3]);
+                            for (int z = 0; z < 4; ++z) y[z] = mul_f16x2(y[z], sw[i / 2]);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                             (dst + step * (kStepRows * 128)) ^ (i << 4)),
+                                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                         : "memory");
                         }
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(&slot_full[j % kSlots]);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&raw_free[st]);
             }
-            cp_async_wait<0>();
+            tiles += (uint32_t)T;
         }
-        if (!ok && ct == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+        cp_async_wait<0>();
+        if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
     } else {  // ---------------------------------------------------------- softmax
         const int m = (warp - 4) >> 2, r = (tid - 128) & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t scol = tmem + lane_base + m * kKeys;
         const uint32_t ocol = tmem + lane_base + 2 * kKeys + m * D;
-        uint32_t ns = 0, tiles = 0;  // S tiles (and last P V) seen, key tiles so far
+        uint32_t ns = 0, no = 0, tiles = 0;  // S and O tiles seen, key tiles so far
         bool ok = true;
         for (Walk w = start(); w.next(a, p); tiles += (uint32_t)(p.t1 - p.t0)) {
             const int T = p.t1 - p.t0, nm = p.rows > 128 ? 2 : 1;
@@ -498,114 +566,130 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (m >= nm) continue;
             const float rs = a.scale_log2 * head_scale(a.c.k_scale, p.h) * pow2i(e);
             float mx = -INFINITY, l = 0.f, alpha = 0.f;
-            float acc[D];
+            uint64_t acc[D / 2];  // pairs of channels
 #pragma unroll
-            for (int c = 0; c < D; ++c) acc[c] = 0.f;
+            for (int c = 0; c < D / 2; ++c) acc[c] = 0ull;
             for (int i = 0; i < T; ++i) {
-                ok = ok && mbar_wait_bounded(&s_full[m], ns & 1);
+                const int t0 = (p.t0 + i) * kKeys;
+                ok = ok && mbar_wait_bounded(&s_full[m], ns++ & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                ++ns;
                 tc::fence_after_sync();
-                const int t0 = (p.t0 + i) * kKeys;
                 const uint32_t tm = tile_mask[(tiles + i) & 3];
                 const bool full = tm == (1u << (kKeys / 16)) - 1u && t0 + kKeys <= lim_warp;
-                if (i > 0) {  // the last tile's O
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t ov[32];
-                        tc::tmem_ld32(ocol + 32 * c, ov);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            acc[32 * c + x] = fmaf(acc[32 * c + x], alpha, __uint_as_float(ov[x]));
-                    }
-                }
                 // the row's largest logit
-                float mt = -INFINITY;
+                float mt = -INFINITY, mt2 = -INFINITY;
+                if (full) {
+                    uint32_t sv[2][32];
+                    tc::tmem_ld32(scol, sv[0]);
 #pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    uint32_t sv[32];
-                    tc::tmem_ld32(scol + 32 * c, sv);
-                    tc::tmem_wait_ld();
-                    if (full) {
+                    for (int c = 0; c < kKeys / 32; ++c) {
+                        tc::tmem_wait_ld();
+                        if (c + 1 < kKeys / 32) tc::tmem_ld32(scol + 32 * (c + 1), sv[(c + 1) & 1]);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) mt = fmaxf(mt, __uint_as_float(sv[x]));
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const int k = 32 * c + x;
-                            if (t0 + k < lim && ((tm >> (k / 16)) & 1u)) mt = fmaxf(mt, __uint_as_float(sv[x]));
+                        for (int x = 0; x < 32; x += 4) {
+                            mt = max3(mt, __uint_as_float(sv[c & 1][x]), __uint_as_float(sv[c & 1][x + 1]));
+                            mt2 = max3(mt2, __uint_as_float(sv[c & 1][x + 2]), __uint_as_float(sv[c & 1][x + 3]));
                         }
+                    }
+                    mt = fmaxf(mt, mt2);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / 16; ++c) {
+                        uint32_t sv[16];
+                        tc::tmem_ld16(scol + 16 * c, sv);
+                        tc::tmem_wait_ld();
+                        const int left = ((tm >> c) & 1u) ? lim - t0 - 16 * c : 0;
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            if (x < left) mt = fmaxf(mt, __uint_as_float(sv[x]));
                     }
                 }
                 mt *= rs;
                 // a whole number, so that every factor 2^(m - m') is exact
                 const float mn = mt > mx ? ceilf(mt) : mx;
-                const float al = mx == -INFINITY ? 0.f : ex2(mx - mn);
+                alpha = mx == -INFINITY ? 0.f : ex2(mx - mn);
                 mx = mn;
                 const float nb = mn == -INFINITY ? 0.f : kShift - mn;
-                float ls[2] = {0.f, 0.f};
+                const uint64_t rs2 = pack2(rs, rs), nb2 = pack2(nb, nb), minus = pack2(-1.f, -1.f);
+                uint64_t ls[2] = {0ull, 0ull};
+                uint32_t sv[2][16];
+                tc::tmem_ld16(scol, sv[0]);
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                for (int c = 0; c < kKeys / 32; ++c) {
-                    uint32_t sv[32];
-                    tc::tmem_ld32(scol + 32 * c, sv);
-                    tc::tmem_wait_ld();
-                    if (!full) {
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t col = scol + 64 * hf + 16 * c;
+                        uint32_t (&x)[16] = sv[c & 1];
+                        tc::tmem_wait_ld();
+                        if (c < 3 || hf == 0) tc::tmem_ld16(col + 16, sv[(c + 1) & 1]);
+                        if (!full) {
+                            const int left = ((tm >> (4 * hf + c)) & 1u) ? lim - t0 - 64 * hf - 16 * c : 0;
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const int k = 32 * c + x;
-                            if (!(t0 + k < lim && ((tm >> (k / 16)) & 1u))) sv[x] = 0xff800000u;
+                            for (int k = 0; k < 16; ++k)
+                                if (k >= left) x[k] = 0xff800000u;
                         }
-                    }
-                    uint32_t pw[32];  // 16 columns of hi, 16 of lo
+                        uint32_t pw[16];  // 8 columns of hi, 8 of lo
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const float p0 = ex2(fmaf(__uint_as_float(sv[2 * x]), rs, nb));
-                        const float p1 = ex2(fmaf(__uint_as_float(sv[2 * x + 1]), rs, nb));
-                        ls[0] += p0;
-                        ls[1] += p1;
-                        pw[x] = pack_f16(p0, p1);
-                        pw[16 + x] = pack_f16(p0 - f16_lo(pw[x]), p1 - f16_hi(pw[x]));
+                        for (int k = 0; k < 8; ++k) {
+                            float p0, p1, l0, l1;
+                            unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), rs2, nb2),
+                                    p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            const uint64_t pp = pack2(p0, p1);
+                            ls[k & 1] = add2(ls[k & 1], pp);
+                            // hi: the leading 11 bits, so that lo = p - hi is exact
+                            const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
+                            const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
+                            unpack2(fma2(pack2(h0, h1), minus, pp), l0, l1);
+                            pw[k] = pack_f16(h0, h1);
+                            pw[8 + k] = pack_f16(l0, l1);
+                        }
+                        tc::tmem_st16(col, pw);
                     }
-                    tc::tmem_st32(scol + 32 * c, pw);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(&p_full[m][hf]);
                 }
-                l = fmaf(l, al, ls[0] + ls[1]);
-                alpha = al;
-                tc::tmem_wait_st();
+                {
+                    float l0, l1;
+                    unpack2(add2(ls[0], ls[1]), l0, l1);
+                    l = fmaf(l, alpha, l0 + l1);
+                }
+                // The tile's O into the row, while the next S is made.
+                ok = mbar_wait_bounded(&o_full[m], no++ & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint64_t alpha2 = pack2(alpha, alpha);
+                uint32_t ov[2][32];
+                tc::tmem_ld32(ocol, ov[0]);
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    tc::tmem_wait_ld();
+                    if (c + 1 < D / 32) tc::tmem_ld32(ocol + 32 * (c + 1), ov[(c + 1) & 1]);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        acc[16 * c + x] = fma2(acc[16 * c + x], alpha2,
+                                               pack2(__uint_as_float(ov[c & 1][2 * x]),
+                                                     __uint_as_float(ov[c & 1][2 * x + 1])));
+                }
                 tc::fence_before_sync();
-                mbar_arrive(&p_full[m]);
             }
-            ok = ok && mbar_wait_bounded(&s_full[m], ns & 1);  // the last P V
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            ++ns;
-            tc::fence_after_sync();
             const bool whole = p.t0 == 0 && p.t1 == p.cnt;
             const float inv = l > 0.f ? head_scale(a.c.v_scale, p.h) / l : (l == 0.f ? 0.f : l);
             const size_t slot = (size_t)(2 * cta + p.slot) * kRows + lrow;
             float *dst = whole ? a.out + orow * D : a.part_o + slot * D;
+            if (row_ok) {
+                const uint64_t f2 = whole ? pack2(inv, inv) : pack2(1.f, 1.f);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t ov[32];
-                tc::tmem_ld32(ocol + 32 * c, ov);
-                tc::tmem_wait_ld();
-                if (row_ok) {
-#pragma unroll
-                    for (int x = 0; x < 32; x += 4) {
-                        float4 v;
-                        v.x = fmaf(acc[32 * c + x], alpha, __uint_as_float(ov[x]));
-                        v.y = fmaf(acc[32 * c + x + 1], alpha, __uint_as_float(ov[x + 1]));
-                        v.z = fmaf(acc[32 * c + x + 2], alpha, __uint_as_float(ov[x + 2]));
-                        v.w = fmaf(acc[32 * c + x + 3], alpha, __uint_as_float(ov[x + 3]));
-                        if (whole) {
-                            v.x *= inv;
-                            v.y *= inv;
-                            v.z *= inv;
-                            v.w *= inv;
-                        }
-                        *reinterpret_cast<float4 *>(dst + 32 * c + x) = v;
-                    }
+                for (int c = 0; c < D; c += 4) {
+                    float4 v;
+                    unpack2(fma2(acc[c / 2], f2, 0ull), v.x, v.y);
+                    unpack2(fma2(acc[c / 2 + 1], f2, 0ull), v.z, v.w);
+                    *reinterpret_cast<float4 *>(dst + c) = v;
                 }
             }
             if (row_ok) {
@@ -615,7 +699,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.lse[orow] = l > 0.f ? (mx - kShift + log2f(l)) * 0.6931471805599453f
                                   : l == 0.f ? -INFINITY : l;
             }
-            tc::fence_before_sync();
         }
         if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
     }
