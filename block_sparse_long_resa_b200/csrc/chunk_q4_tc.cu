@@ -734,12 +734,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int W = sh_w, G = sh_ctas;
         const int q0 = (int)((((long long)p.ustart + 1) * G - 1) / W);
         const int q1 = (int)((((long long)p.ustart + p.cnt) * G - 1) / W);
+        const int odd = entry_of(q0, W, G) < p.ustart ? 1 : 0;  // only q0's share can begin before the unit
         const int k = q1 - q0 + 1, mine_i = cta - q0;
         const int r0 = (int)((long long)p.rows * mine_i / k), r1 = (int)((long long)p.rows * (mine_i + 1) / k);
         const float vg = head_scale(a.c.v_scale, p.h);
         for (int lrow = r0 + warp; lrow < r1; lrow += kThreads / 32) {
             auto slot_of = [&](int q) -> size_t {
-                return (size_t)(2 * q + (entry_of(q, W, G) >= p.ustart ? 0 : 1)) * kRows + lrow;
+                return (size_t)(2 * q + (q == q0 ? odd : 0)) * kRows + lrow;
             };
             float ms = -INFINITY;
             for (int q = q0 + lane; q <= q1; q += 32) ms = fmaxf(ms, __ldcg(&a.part_ml[slot_of(q)]).x);

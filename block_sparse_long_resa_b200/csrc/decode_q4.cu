@@ -34,7 +34,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 4;
-constexpr int kStep = 32;          // positions a warp takes at a time
 constexpr int kMinBlocks = 4;      // blocks a CTA takes at least, when there are few
 constexpr float kShift = 13.f;     // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 2.f;      // growth of the maximum tolerated before rescaling
@@ -135,9 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kWords = D / 32;   // 32-bit words of codes a lane takes per K row
     constexpr int kRows = NT * 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long sh_sum[kWarps + 1];
-    __shared__ int sh_unit;
-    __shared__ long long sh_first;
+    __shared__ int sh_sum[kWarps], sh_unit, sh_first;
     __shared__ uint32_t sh_last;
 
     pdl_launch_next();
@@ -183,17 +180,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Prefix sums of the units' blocks: thread t sums units [t * per, ...).
     const int per = (units + kThreads - 1) / kThreads;
     const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
-    long long mine = 0;
+    int mine = 0;
     for (int u = u_lo; u < u_hi; ++u) mine += unit_of(u, false).cnt;
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
     if (lane == 31) sh_sum[warp] = incl;
     __syncthreads();
-    long long before = 0, W = 0;
+    int before = 0, W = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += sh_sum[w];
@@ -201,10 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     incl += before;
     // CTAs that take work: at least kMinBlocks entries each
-    const long long G = max(1LL, min((long long)gridDim.x, (W + kMinBlocks - 1) / kMinBlocks));
-    const long long x0 = cta < G ? W * cta / G : W, x1 = cta < G ? W * (cta + 1) / G : W;
+    const int G = max(1, min((int)gridDim.x, (W + kMinBlocks - 1) / kMinBlocks));
+    auto entry_of = [&](int q) -> int { return q < G ? (int)((long long)W * q / G) : W; };
+    const int x0 = entry_of(cta), x1 = entry_of(cta + 1);
     if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
-        long long s = incl - mine;
+        int s = incl - mine;
         for (int u = u_lo; u < u_hi; ++u) {
             const int k = unit_of(u, false).cnt;
             if (x0 < s + k) {
@@ -218,16 +216,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
 
     int u = x0 < x1 ? sh_unit : 0;
-    long long ustart = x0 < x1 ? sh_first : 0;
+    int ustart = x0 < x1 ? sh_first : 0;
     const int sub_shift = a.bs == 64 ? 2 : a.bs == 32 ? 1 : 0;  // tiles a block
     uint8_t *ring = smem + (size_t)warp * kStages * SM::kStage;
     const uint32_t ring_s = smem_u32(ring);
 
-    for (long long x = x0; x < x1; ++u) {
+    for (int x = x0; x < x1; ++u) {
         const Unit un = unit_of(u, false);
         if (un.cnt == 0) continue;
-        const long long uend = ustart + un.cnt;
-        const int j0 = (int)(x - ustart), j1 = (int)(min(x1, uend) - ustart);  // entries of this piece
+        const int uend = ustart + un.cnt;
+        const int j0 = x - ustart, j1 = min(x1, uend) - ustart;  // entries of this piece
         const int b = un.b, h = un.h, L = un.L;
         const int rows_all = a.block_idx ? a.g : un.n * a.g;
         const int base_pos = a.block_idx ? 0 : L - un.n;  // row rho sees positions <= base_pos + rho / g
@@ -493,12 +491,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bl[k][n][1] = movmatrix_trans(l1);
                 }
             }
-            // O^T += V^T P^T
+            // O^T += V^T P^T.  The matrix unit truncates when it adds to its
+            // accumulator; over a long sequence that would be a bias, so a step's
+            // products start from zero and are added to the row in fp32 here.
+            uint32_t sv[2][2];  // scales of the token pairs (2c, 2c+1), (2c+8, 2c+9)
+            uint32_t w[2][4][D / 64];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint32_t vt = st + SM::kV + k * SM::kCodes;
-                uint32_t sv[2];  // scales of the token pairs (2c, 2c+1), (2c+8, 2c+9)
-                uint32_t w[4][D / 64];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int t0 = 2 * c + 8 * i;
@@ -508,33 +508,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                         s0 = t0 < ntok[k] ? s0 : 0u;
                         s1 = t0 + 1 < ntok[k] ? s1 : 0u;
                     }
-                    sv[i] = e4m3x2_to_f16(s0 | (s1 << 8));
+                    sv[k][i] = e4m3x2_to_f16(s0 | (s1 << 8));
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int t1 = t0 + j;
                         if (D == 128)
-                            lds_words<D / 64>(w[2 * i + j], vt + v_chunk<D>(t1, r >> 1) + (r & 1) * 8);
+                            lds_words<D / 64>(w[k][2 * i + j], vt + v_chunk<D>(t1, r >> 1) + (r & 1) * 8);
                         else
-                            lds_words<D / 64>(w[2 * i + j], vt + v_chunk<D>(t1, r >> 2) + (r & 3) * 4);
+                            lds_words<D / 64>(w[k][2 * i + j], vt + v_chunk<D>(t1, r >> 2) + (r & 3) * 4);
                     }
                 }
+            }
 #pragma unroll
-                for (int wi = 0; wi < D / 64; ++wi) {
-                    uint32_t e[4][4];
+            for (int wi = 0; wi < D / 64; ++wi) {
+                // codes of two tokens side by side: even channels in e0, odd ones in e1
+                uint32_t e0[2][2][4], e1[2][2][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) e2m1x8_to_f16(w[i][wi], e[i]);
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a0 = mul_f16x2(__byte_perm(e[0][j], e[1][j], 0x5410), sv[0]);
-                        const uint32_t a1 = mul_f16x2(__byte_perm(e[0][j], e[1][j], 0x7632), sv[0]);
-                        const uint32_t a2 = mul_f16x2(__byte_perm(e[2][j], e[3][j], 0x5410), sv[1]);
-                        const uint32_t a3 = mul_f16x2(__byte_perm(e[2][j], e[3][j], 0x7632), sv[1]);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t t0 = w[k][2 * i][wi], t1 = w[k][2 * i + 1][wi];
+                        e2m1x8_to_f16((t0 & 0x0f0f0f0fu) | ((t1 << 4) & 0xf0f0f0f0u), e0[k][i]);
+                        e2m1x8_to_f16(((t0 >> 4) & 0x0f0f0f0fu) | (t1 & 0xf0f0f0f0u), e1[k][i]);
+                    }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float part[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t a0 = mul_f16x2(e0[k][0][j], sv[k][0]), a1 = mul_f16x2(e1[k][0][j], sv[k][0]);
+                        const uint32_t a2 = mul_f16x2(e0[k][1][j], sv[k][1]), a3 = mul_f16x2(e1[k][1][j], sv[k][1]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma_f16(o[4 * wi + j][n], a0, a1, a2, a3, bh[k][n][0], bh[k][n][1]);
-                            mma_f16(o[4 * wi + j][n], a0, a1, a2, a3, bl[k][n][0], bl[k][n][1]);
+                            mma_f16(part[n], a0, a1, a2, a3, bh[k][n][0], bh[k][n][1]);
+                            mma_f16(part[n], a0, a1, a2, a3, bl[k][n][0], bl[k][n][1]);
                         }
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[4 * wi + j][n][x] += part[n][x];
                 }
             }
             __syncwarp();
@@ -581,12 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int qr = rho;
             return ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
         };
-        // partial slot of CTA q for this unit: 2q when its share starts in the
-        // unit (its first piece), else 2q + 1 (its last piece)
-        auto slot_of = [&](long long q) -> size_t {
-            return (size_t)(2 * q + (W * q / G >= ustart ? 0 : 1));
-        };
-        const size_t slot = whole ? 0 : slot_of(cta);
+        // Partial slot of this CTA: 2 cta for its first piece, 2 cta + 1 for a later one.
+        const int slot = 2 * cta + (x == x0 ? 0 : 1);
         for (int e = tid; e < rows_all * D; e += kThreads) {
             const int rho = e / D, ch = e % D;
             float ms = -INFINITY, ls = 0.f, os = 0.f;
@@ -602,44 +613,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (whole) {
                 const size_t orow = orow_of(rho);
-                a.out[orow * D + ch] = ls > 0.f ? os / ls * vg : 0.f;
+                a.out[orow * D + ch] = ls == 0.f ? 0.f : os / ls * vg;
                 if (a.lse && ch == 0)
-                    a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2 : -INFINITY;
+                    a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2 : ls == 0.f ? -INFINITY : ls;
             } else {
-                a.part_o[(slot * kMaxGroup + rho) * D + ch] = os;
+                a.part_o[((size_t)slot * kMaxGroup + rho) * D + ch] = os;
                 if (ch == 0) a.part_ml[slot * kMaxGroup + rho] = make_float2(ms, ls);
             }
         }
         if (!whole) {
             __threadfence();
             __syncthreads();
-            // CTAs whose shares meet the unit
-            const long long q0 = ((ustart + 1) * G - 1) / W, q1 = (uend * G - 1) / W;
+            // CTAs q0 .. q1 whose shares meet the unit; only q0's can begin before it
+            const int q0 = (int)((((long long)ustart + 1) * G - 1) / W), q1 = (int)(((long long)uend * G - 1) / W);
+            const int parts = q1 - q0 + 1, odd = entry_of(q0) < ustart ? 1 : 0;
             if (tid == 0) {
                 const uint32_t k = atomicAdd(&a.tickets[u], 1u);
-                sh_last = k == (uint32_t)(q1 - q0);
+                sh_last = k == (uint32_t)(parts - 1);
                 if (sh_last) a.tickets[u] = 0u;
             }
             __syncthreads();
             if (sh_last) {
                 __threadfence();
-                for (int e = tid; e < rows_all * D; e += kThreads) {
-                    const int rho = e / D, ch = e % D;
-                    float ms = -INFINITY, ls = 0.f, os = 0.f;
-                    for (long long q = q0; q <= q1; ++q)
+                // each part's weight per row, then the weighted sum, four channels a thread
+                float *wt = reinterpret_cast<float *>(smem);  // [rows][parts]
+                float *wsum = wt + rows_all * parts;          // [rows]
+                auto slot_of = [&](int q) -> int { return 2 * (q0 + q) + (q == 0 ? odd : 0); };
+                for (int rho = warp; rho < rows_all; rho += kWarps) {
+                    float ms = -INFINITY, ls = 0.f;
+                    for (int q = lane; q < parts; q += 32)
                         ms = fmaxf(ms, __ldcg(&a.part_ml[slot_of(q) * kMaxGroup + rho]).x);
-                    if (ms != -INFINITY)
-                        for (long long q = q0; q <= q1; ++q) {
-                            const size_t sl = slot_of(q) * kMaxGroup + rho;
-                            const float2 ml = __ldcg(&a.part_ml[sl]);
-                            const float f2 = ex2(ml.x - ms);
-                            ls += ml.y * f2;
-                            os += __ldcg(&a.part_o[sl * D + ch]) * f2;
-                        }
-                    const size_t orow = orow_of(rho);
-                    a.out[orow * D + ch] = ls > 0.f ? os / ls * vg : 0.f;
-                    if (a.lse && ch == 0)
-                        a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2 : -INFINITY;
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o2));
+                    for (int q = lane; q < parts; q += 32) {
+                        const float2 ml = __ldcg(&a.part_ml[slot_of(q) * kMaxGroup + rho]);
+                        const float f2 = ms == -INFINITY ? 0.f : ex2(ml.x - ms);
+                        wt[rho * parts + q] = f2;
+                        ls += ml.y * f2;
+                    }
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o2);
+                    if (lane == 0) {
+                        wsum[rho] = ls > 0.f ? vg / ls : (ls == 0.f ? 0.f : ls);
+                        if (a.lse)
+                            a.lse[orow_of(rho)] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2
+                                                  : ls == 0.f ? -INFINITY : ls;
+                    }
+                }
+                __syncthreads();
+                for (int e = tid; e < rows_all * (D / 4); e += kThreads) {
+                    const int rho = e / (D / 4), c4 = e % (D / 4);
+                    float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int q = 0; q < parts; ++q) {
+                        const float f2 = wt[rho * parts + q];
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                                                    a.part_o + ((size_t)slot_of(q) * kMaxGroup + rho) * D) + c4);
+                        os.x += v.x * f2;
+                        os.y += v.y * f2;
+                        os.z += v.z * f2;
+                        os.w += v.w * f2;
+                    }
+                    const float f3 = wsum[rho];
+                    reinterpret_cast<float4 *>(a.out + orow_of(rho) * D)[c4] =
+                        make_float4(os.x * f3, os.y * f3, os.z * f3, os.w * f3);
                 }
             }
         }

@@ -143,7 +143,8 @@ resa_status_t resa_sparse_decode_q4(const resa_config_t *cfg, const resa_cache_q
     RESA_TRY(check_config(cfg, &s));
     RESA_TRY(check_cache_q4(cache, &s, false, &c));
     if (!q || !block_idx || !block_cnt || !out) return RESA_ERR_NULL;
-    if (max_topk < 0 || max_topk == INT32_MAX) return RESA_ERR_RANGE;
+    if (max_topk < 0 || (long long)s.batch * s.hkv * ((long long)max_topk + 1) > 0x7fffffffLL)
+        return RESA_ERR_RANGE;
     if (!aligned16(q) || !aligned16(out) || !aligned4(block_idx) || !aligned4(block_cnt) ||
         !aligned4(lse_opt))
         return RESA_ERR_UNSUPPORTED;
@@ -171,9 +172,8 @@ resa_status_t resa_attention_q4(const resa_config_t *cfg, const resa_cache_q4_t 
         return RESA_ERR_UNSUPPORTED;
     const WsLayout w = layout_of(s, f * s.g <= kMaxGroup ? 0 : f);
     RESA_TRY(check_ws(ws, ws_bytes, w));
-    if ((long long)s.batch * s.hkv * rect_row_groups(f, s.g) * (((long long)s.max_pages * s.bs + 127) / 128) >
-        0x7fffffffLL)
-        return RESA_ERR_RANGE;
+    if ((long long)s.batch * s.hkv * rect_row_groups(f, s.g) > 0x7fffffffLL / s.max_pages)
+        return RESA_ERR_RANGE;  // entries of work are counted in 32 bits
     uint32_t *err = at<uint32_t>(ws, w.err);
     if (f * s.g <= kMaxGroup)
         return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
