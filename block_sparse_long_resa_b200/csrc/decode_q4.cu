@@ -31,15 +31,16 @@
 namespace resa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
-constexpr int kMinBlocks = 4;      // blocks a CTA takes at least, when there are few
+template <int D, int NT>
+struct Q4Warps {
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 4 : 4;
+};
 constexpr float kShift = 13.f;     // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 2.f;      // growth of the maximum tolerated before rescaling
 
-template <int D>
+template <int D, int NT>
 struct Q4Smem {
+    static constexpr int kWarps = Q4Warps<D, NT>::kWarps, kStages = Q4Warps<D, NT>::kStages;
     static constexpr int kCodes = kTileRows * D / 2;   // one tile's K or V codes
     static constexpr int kScales = kTileRows * D / 16; // and group scales
     static constexpr int kV = 2 * kCodes;              // offsets inside a stage (two tiles)
@@ -128,13 +129,17 @@ struct DecodeQ4Args {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     decode_q4_kernel(const __grid_constant__ DecodeQ4Args a) {
-    using SM = Q4Smem<D>;
+    using SM = Q4Smem<D, NT>;
+    constexpr int kWarps = SM::kWarps, kStages = SM::kStages, kThreads = 32 * kWarps;
     constexpr int kWords = D / 32;   // 32-bit words of codes a lane takes per K row
     constexpr int kRows = NT * 8;
+    constexpr int kItems = (kRows * (D / 4) + kThreads - 1) / kThreads;  // 4 channels each
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int sh_sum[kWarps], sh_unit, sh_first;
+    __shared__ int4 sh_units[kThreads];  // (blocks, length, fresh tokens, row) when they fit
+    __shared__ float2 sh_ml[kRows];  // a row's maximum and sum
     __shared__ uint32_t sh_last;
 
     pdl_launch_next();
@@ -149,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit x;
         x.b = u / a.hkv;
         x.h = u - x.b * a.hkv;
+        const bool dense = a.block_idx == nullptr;
+        const int listed = dense ? 0 : a.block_cnt[u];
         x.n = a.n_new ? a.n_new[x.b] : a.f;
         x.cnt = 0;
         x.L = 0;
@@ -158,7 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t *err = report && x.h == 0 ? a.err : nullptr;
         x.row = cache_row(a.rm, x.b, err);
         x.L = row_seq_len(a.seq_len, x.row);
-        const bool dense = a.block_idx == nullptr;
         if (x.row < 0 || x.L < (dense ? 0 : 1) || (long long)x.L > (long long)a.max_pages * a.bs) {
             set_error(err, RESA_DEVERR_SEQ_LEN);
             x.live = !dense;
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             x.cnt = (x.L + a.bs - 1) / a.bs;
         } else {
-            x.cnt = max(0, min(a.block_cnt[u], a.max_topk + 1));
+            x.cnt = max(0, min(listed, a.max_topk + 1));
         }
         return x;
     };
@@ -181,7 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = (units + kThreads - 1) / kThreads;
     const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
     int mine = 0;
-    for (int u = u_lo; u < u_hi; ++u) mine += unit_of(u, false).cnt;
+    for (int u = u_lo; u < u_hi; ++u) {
+        const Unit x = unit_of(u, false);
+        mine += x.cnt;
+        if (per == 1) sh_units[u] = make_int4(x.cnt, x.L, x.n, x.row);
+    }
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -197,14 +207,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         W += sh_sum[w];
     }
     incl += before;
-    // CTAs that take work: at least kMinBlocks entries each
-    const int G = max(1, min((int)gridDim.x, (W + kMinBlocks - 1) / kMinBlocks));
+    // CTAs that take work: enough for a step of every warp each
+    const int least = max(1, 32 * kWarps / a.bs);
+    const int G = max(1, min((int)gridDim.x, (W + least - 1) / least));
     auto entry_of = [&](int q) -> int { return q < G ? (int)((long long)W * q / G) : W; };
     const int x0 = entry_of(cta), x1 = entry_of(cta + 1);
     if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
         int s = incl - mine;
         for (int u = u_lo; u < u_hi; ++u) {
-            const int k = unit_of(u, false).cnt;
+            const int k = per == 1 ? mine : unit_of(u, false).cnt;
             if (x0 < s + k) {
                 sh_unit = u;
                 sh_first = s;
@@ -222,7 +233,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring_s = smem_u32(ring);
 
     for (int x = x0; x < x1; ++u) {
-        const Unit un = unit_of(u, false);
+        Unit un;
+        if (per == 1) {
+            const int4 x4 = sh_units[u];
+            un.b = u / a.hkv;
+            un.h = u - un.b * a.hkv;
+            un.cnt = x4.x;
+            un.L = x4.y;
+            un.n = x4.z;
+            un.row = x4.w;
+        } else {
+            un = unit_of(u, false);
+        }
         if (un.cnt == 0) continue;
         const int uend = ustart + un.cnt;
         const int j0 = x - ustart, j1 = min(x1, uend) - ustart;  // entries of this piece
@@ -241,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Tiles' places 16 steps at a time, one a lane (lane 2i + k: tile k of
         // step 16 w + i), with the next window already in flight: byte-tile
         // index of the cache (page, head, tile in block), position, validity.
-        auto load_win = [&](int w, long long &tile, int &pos) {
+        auto load_win = [&](int w, int &tile, int &pos) {
             const int t = w * 16 + (lane >> 1);
             const int e = 2 * (warp + kWarps * t) + (lane & 1);
             tile = -1;
@@ -260,22 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 set_error(a.err, RESA_DEVERR_PAGE);
                 return;
             }
-            tile = ((((long long)page * a.hkv + h) << sub_shift) | sub);
+            tile = ((page * a.hkv + h) << sub_shift) | sub;
         };
-        long long win_tile[2];
-        int win_pos[2];
+        int win_tile[2], win_pos[2];
         load_win(0, win_tile[0], win_pos[0]);
         load_win(1, win_tile[1], win_pos[1]);
-        // The loads of step t (its window is 0 or 1 ahead of the consumer's).
+        // Tile k of step t (its window is 0 or 1 ahead of the consumer's).  A branch, so
+        // that the next window's loads are not waited for before they are used.
         int win_base = 0;  // window held in slot 0
-        auto tile_at = [&](int t, int k, int &pos) -> long long {
-            const int w = (t >> 4) - win_base, src = 2 * (t & 15) + k;
-            const long long t0 = __shfl_sync(0xffffffffu, win_tile[0], src);
-            const long long t1 = __shfl_sync(0xffffffffu, win_tile[1], src);
-            const int p0 = __shfl_sync(0xffffffffu, win_pos[0], src);
-            const int p1 = __shfl_sync(0xffffffffu, win_pos[1], src);
-            pos = w ? p1 : p0;
-            return w ? t1 : t0;
+        auto tile_at = [&](int t, int k) -> int {
+            const int src = 2 * (t & 15) + k;
+            if ((t >> 4) == win_base) return __shfl_sync(0xffffffffu, win_tile[0], src);
+            return __shfl_sync(0xffffffffu, win_tile[1], src);
         };
         auto issue = [&](int t) {
             if (t < nsteps) {
@@ -284,8 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr int kPerRow = D / 32;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    int pos;
-                    const long long tile = tile_at(t, k, pos);
+                    const int tile = tile_at(t, k);
                     if (tile < 0) continue;
                     const uint8_t *gk = a.c.k + (size_t)tile * SM::kCodes;
                     const uint8_t *gv = a.c.v + (size_t)tile * SM::kCodes;
@@ -371,7 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int tp[2];
             bool there[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) there[k] = tile_at(t, k, tp[k]) >= 0;
+            for (int k = 0; k < 2; ++k) {  // of the window in slot 0
+                there[k] = __shfl_sync(0xffffffffu, win_tile[0], 2 * (t & 15) + k) >= 0;
+                tp[k] = __shfl_sync(0xffffffffu, win_pos[0], 2 * (t & 15) + k);
+            }
             issue(t + kStages - 1);
             cp_async_wait<kStages - 1>();
             __syncwarp();
@@ -442,21 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (!there[k] || pos >= lim[n][k2]) s[k][n][2 * hh + k2] = -INFINITY;
                             }
                     }
-                    float x = fmaxf(fmaxf(s[0][n][k2], s[0][n][2 + k2]), fmaxf(s[1][n][k2], s[1][n][2 + k2]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    mt[n][k2] = x * row_scale[n][k2];
-                    grow |= mt[n][k2] > m[n][k2] + kSlack;
+                    mt[n][k2] = fmaxf(fmaxf(s[0][n][k2], s[0][n][2 + k2]), fmaxf(s[1][n][k2], s[1][n][2 + k2]));
+                    grow |= mt[n][k2] * row_scale[n][k2] > m[n][k2] + kSlack;
                 }
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__any_sync(0xffffffffu, grow)) {  // the columns' maxima only when one may grow
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float alpha[2];
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
+                        float x = mt[n][k2];
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         // a whole number, so that every factor 2^(m - m') is exact
-                        const float mn = ceilf(fmaxf(m[n][k2], mt[n][k2]));
+                        const float mn = ceilf(fmaxf(m[n][k2], x * row_scale[n][k2]));
                         alpha[k2] = m[n][k2] == -INFINITY ? 0.f : ex2(m[n][k2] - mn);
                         m[n][k2] = mn;
                         l[n][k2] *= alpha[k2];
@@ -570,10 +590,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l[n][k2] += __shfl_xor_sync(0xffffffffu, l[n][k2], 16);
             }
         __syncthreads();  // every ring is drained
-        // Merge the warps: states to shared memory, [warp][row] and [warp][row][D].
+        // Merge the warps.  A row's channels lie in shared memory (and in the partials) in
+        // the order of the lanes, channel r * D/8 + 2 t2 + z at place 16 t2 + 2 r + z, and
+        // rows are padded by 4, so that a store's lanes meet all banks.
+        constexpr int kRow = D + 4;
         float *wm = reinterpret_cast<float *>(smem);
-        float *wl = wm + kWarps * kRows;
-        float *wo = wl + kWarps * kRows;
+        float *wl = wm + kWarps * kRows, *wf = wl + kWarps * kRows;
+        float *wo = wf + kWarps * kRows;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -583,42 +606,66 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wm[warp * kRows + rho] = m[n][k2];
                     wl[warp * kRows + rho] = l[n][k2];
                 }
-                float *dst = wo + ((size_t)warp * kRows + rho) * D + r * (D / 8);
+                float *dst = wo + (warp * kRows + rho) * kRow + 2 * r;
 #pragma unroll
                 for (int t2 = 0; t2 < D / 16; ++t2)
-                    *reinterpret_cast<float2 *>(dst + 2 * t2) = make_float2(o[t2][n][k2], o[t2][n][2 + k2]);
+                    *reinterpret_cast<float2 *>(dst + 16 * t2) = make_float2(o[t2][n][k2], o[t2][n][2 + k2]);
             }
+        __syncthreads();
+        // Each row's maximum and sum, and the warps' factors: a warp a row, a lane a warp.
+        // (From here on the code runs once, from a cold instruction cache: loops are kept
+        // short rather than unrolled.)
+        for (int rho = warp; rho < rows_all; rho += kWarps) {
+            const int at = lane * kRows + rho;
+            const float mw = lane < kWarps ? wm[at] : -INFINITY;
+            float ms = mw;
+#pragma unroll
+            for (int o2 = 8; o2 > 0; o2 >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o2));
+            const float f2 = ms == -INFINITY ? 0.f : ex2(mw - ms);
+            float ls = lane < kWarps ? wl[at] * f2 : 0.f;
+#pragma unroll
+            for (int o2 = 8; o2 > 0; o2 >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o2);
+            if (lane < kWarps) wf[at] = f2;
+            if (lane == 0) sh_ml[rho] = make_float2(ms, ls);
+        }
         __syncthreads();
         const bool whole = j0 == 0 && j1 == un.cnt;
         const float vg = head_scale(a.c.v_scale, h);
-        const float kLn2 = 0.6931471805599453f;
         auto orow_of = [&](int rho) -> size_t {
             const int qr = rho;
             return ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
         };
         // Partial slot of this CTA: 2 cta for its first piece, 2 cta + 1 for a later one.
         const int slot = 2 * cta + (x == x0 ? 0 : 1);
-        for (int e = tid; e < rows_all * D; e += kThreads) {
-            const int rho = e / D, ch = e % D;
-            float ms = -INFINITY, ls = 0.f, os = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) ms = fmaxf(ms, wm[w * kRows + rho]);
-            if (ms != -INFINITY) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f2 = ex2(wm[w * kRows + rho] - ms);
-                    ls += wl[w * kRows + rho] * f2;
-                    os += wo[((size_t)w * kRows + rho) * D + ch] * f2;
-                }
+        // four places of a row: channels ch, ch + 1 and ch + D/8, ch + D/8 + 1
+        auto store_out = [&](int rho, int p4, float4 v) {
+            float *dst = a.out + orow_of(rho) * D + (p4 % 4) * (D / 4) + (p4 / 4) * 2;
+            *reinterpret_cast<float2 *>(dst) = make_float2(v.x, v.y);
+            *reinterpret_cast<float2 *>(dst + D / 8) = make_float2(v.z, v.w);
+        };
+        auto lse_of = [&](float ms, float ls) -> float {
+            return ls > 0.f ? (ms - kShift + log2f(ls)) * 0.6931471805599453f : ls == 0.f ? -INFINITY : ls;
+        };
+        for (int e = tid; e < rows_all * (D / 4); e += kThreads) {
+            const int rho = e / (D / 4), p4 = e % (D / 4);
+            float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int w = 0; w < kWarps; ++w) {
+                const float f2 = wf[w * kRows + rho];
+                const float4 v = *reinterpret_cast<const float4 *>(wo + (w * kRows + rho) * kRow + 4 * p4);
+                os.x += v.x * f2;
+                os.y += v.y * f2;
+                os.z += v.z * f2;
+                os.w += v.w * f2;
             }
+            const float2 ml = sh_ml[rho];
             if (whole) {
-                const size_t orow = orow_of(rho);
-                a.out[orow * D + ch] = ls == 0.f ? 0.f : os / ls * vg;
-                if (a.lse && ch == 0)
-                    a.lse[orow] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2 : ls == 0.f ? -INFINITY : ls;
+                const float f2 = ml.y == 0.f ? 0.f : vg / ml.y;
+                store_out(rho, p4, make_float4(os.x * f2, os.y * f2, os.z * f2, os.w * f2));
+                if (a.lse && p4 == 0) a.lse[orow_of(rho)] = lse_of(ml.x, ml.y);
             } else {
-                a.part_o[((size_t)slot * kMaxGroup + rho) * D + ch] = os;
-                if (ch == 0) a.part_ml[slot * kMaxGroup + rho] = make_float2(ms, ls);
+                reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * kMaxGroup + rho) * D)[p4] = os;
+                if (p4 == 0) a.part_ml[slot * kMaxGroup + rho] = ml;
             }
         }
         if (!whole) {
@@ -635,48 +682,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncthreads();
             if (sh_last) {
                 __threadfence();
-                // each part's weight per row, then the weighted sum, four channels a thread
-                float *wt = reinterpret_cast<float *>(smem);  // [rows][parts]
-                float *wsum = wt + rows_all * parts;          // [rows]
-                auto slot_of = [&](int q) -> int { return 2 * (q0 + q) + (q == 0 ? odd : 0); };
+                // All parts at once into shared memory (as many as fit), while their
+                // weights are worked out; then four places a thread.
+                float *wt = reinterpret_cast<float *>(smem);  // [rows][parts] weights
+                const int wt_bytes = (rows_all * parts * 4 + 15) & ~15;
+                float *po = reinterpret_cast<float *>(smem + wt_bytes);
+                const int part_floats = rows_all * D;
+                const int cap = (SM::kRing - wt_bytes) / (part_floats * 4);
+                const float *src0 = a.part_o + (size_t)(2 * q0 + odd) * kMaxGroup * D;
+                const float *src = a.part_o + (size_t)(2 * q0) * kMaxGroup * D;
+                const float2 *ml0 = a.part_ml + (2 * q0 + odd) * kMaxGroup, *mls = a.part_ml + 2 * q0 * kMaxGroup;
+                auto fetch = [&](int from) {
+                    for (int q = from + warp; q < min(parts, from + cap); q += kWarps) {
+                        const float *g = q == 0 ? src0 : src + (size_t)q * (2 * kMaxGroup * D);
+                        const uint32_t dst = smem_u32(po + (q - from) * part_floats);
+#pragma unroll 1
+                        for (int i = lane; i < part_floats / 4; i += 32) cp_async16_s(dst + i * 16, g + i * 4);
+                    }
+                    cp_async_commit();
+                };
+                fetch(0);
                 for (int rho = warp; rho < rows_all; rho += kWarps) {
                     float ms = -INFINITY, ls = 0.f;
-                    for (int q = lane; q < parts; q += 32)
-                        ms = fmaxf(ms, __ldcg(&a.part_ml[slot_of(q) * kMaxGroup + rho]).x);
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, o2));
                     for (int q = lane; q < parts; q += 32) {
-                        const float2 ml = __ldcg(&a.part_ml[slot_of(q) * kMaxGroup + rho]);
-                        const float f2 = ms == -INFINITY ? 0.f : ex2(ml.x - ms);
-                        wt[rho * parts + q] = f2;
-                        ls += ml.y * f2;
+                        const float2 ml = __ldcg((q == 0 ? ml0 : mls + q * 2 * kMaxGroup) + rho);
+                        wt[rho * parts + q] = ml.x;
+                        const float mn = fmaxf(ms, ml.x);
+                        ls = mn == -INFINITY ? 0.f : ls * ex2(ms - mn) + ml.y * ex2(ml.x - mn);
+                        ms = mn;
                     }
+                    float mt = ms;
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o2));
+                    ls = mt == -INFINITY ? 0.f : ls * ex2(ms - mt);
 #pragma unroll
                     for (int o2 = 16; o2 > 0; o2 >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o2);
-                    if (lane == 0) {
-                        wsum[rho] = ls > 0.f ? vg / ls : (ls == 0.f ? 0.f : ls);
-                        if (a.lse)
-                            a.lse[orow_of(rho)] = ls > 0.f ? (ms - kShift + log2f(ls)) * kLn2
-                                                  : ls == 0.f ? -INFINITY : ls;
+                    const float f3 = ls == 0.f ? 0.f : vg / ls;
+                    for (int q = lane; q < parts; q += 32) {
+                        float &x = wt[rho * parts + q];
+                        x = mt == -INFINITY ? 0.f : ex2(x - mt) * f3;
+                    }
+                    if (a.lse && lane == 0) a.lse[orow_of(rho)] = lse_of(mt, ls);
+                }
+                float4 os[kItems];
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) os[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int from = 0; from < parts; from += cap) {
+                    if (from > 0) {
+                        __syncthreads();
+                        fetch(from);
+                    }
+                    cp_async_wait<0>();
+                    __syncthreads();
+                    const int n = min(cap, parts - from);
+#pragma unroll
+                    for (int i = 0; i < kItems; ++i) {
+                        const int e = tid + i * kThreads;
+                        if (e * 4 < part_floats) {
+                            const float *w = wt + e / (D / 4) * parts + from;
+#pragma unroll 4
+                            for (int q = 0; q < n; ++q) {
+                                const float f2 = w[q];
+                                const float4 v = *reinterpret_cast<const float4 *>(po + q * part_floats + 4 * e);
+                                os[i].x += v.x * f2;
+                                os[i].y += v.y * f2;
+                                os[i].z += v.z * f2;
+                                os[i].w += v.w * f2;
+                            }
+                        }
                     }
                 }
-                __syncthreads();
-                for (int e = tid; e < rows_all * (D / 4); e += kThreads) {
-                    const int rho = e / (D / 4), c4 = e % (D / 4);
-                    float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int q = 0; q < parts; ++q) {
-                        const float f2 = wt[rho * parts + q];
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                                                    a.part_o + ((size_t)slot_of(q) * kMaxGroup + rho) * D) + c4);
-                        os.x += v.x * f2;
-                        os.y += v.y * f2;
-                        os.z += v.z * f2;
-                        os.w += v.w * f2;
-                    }
-                    const float f3 = wsum[rho];
-                    reinterpret_cast<float4 *>(a.out + orow_of(rho) * D)[c4] =
-                        make_float4(os.x * f3, os.y * f3, os.z * f3, os.w * f3);
+#pragma unroll
+                for (int i = 0; i < kItems; ++i) {
+                    const int e = tid + i * kThreads;
+                    if (e * 4 < part_floats) store_out(e / (D / 4), e % (D / 4), os[i]);
                 }
             }
         }
@@ -687,6 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Units without any block: zeros and -inf, and the errors of every unit.
     for (int u = cta; u < units; u += gridDim.x) {
+        if (per == 1 && sh_units[u].x > 0) continue;
         const Unit x = unit_of(u, tid == 0);
         if (x.cnt > 0 || !x.live) continue;
         const size_t o = (size_t)x.b * a.f * a.hq + (size_t)x.h * a.g;  // sparse: f = 1
@@ -697,12 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int NT>
 cudaError_t launch_t(const DecodeQ4Args &a, int ctas, cudaStream_t st) {
-    constexpr int merge = kWarps * NT * 8 * (D + 2) * 4;
-    constexpr int smem = Q4Smem<D>::kRing > merge ? Q4Smem<D>::kRing : merge;
+    using SM = Q4Smem<D, NT>;
+    constexpr int merge = SM::kWarps * NT * 8 * (D + 4 + 3) * 4;
+    constexpr int smem = SM::kRing > merge ? SM::kRing : merge;
     static std::atomic<int> done[64];
     cudaError_t e = ensure_smem(decode_q4_kernel<D, NT>, smem, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_q4_kernel<D, NT>, dim3(ctas), dim3(kThreads), smem, st, a);
+    return launch_pdl(decode_q4_kernel<D, NT>, dim3(ctas), dim3(32 * SM::kWarps), smem, st, a);
 }
 
 }  // namespace

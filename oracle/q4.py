@@ -83,7 +83,7 @@ def rotate(x, pos, inv_freq, rot, interleaved, mscale=1.0):
 
 def attention(q, k, v, limit, scale):
     """q [rows, d] against k, v [n, d] (float64); row i sees the first limit[i] of them.  Returns
-    the output, the log-sum-exp, sum p |v| and the largest sum |q k| of a row's keys."""
+    the output, the log-sum-exp, sum p |v|, the largest sum |q k| of a row's keys and sum |v|."""
     x = q @ k.T * scale
     mag = (np.abs(q) @ np.abs(k).T * scale).max(-1, initial=0.0)
     x = np.where(np.arange(k.shape[0])[None] < np.asarray(limit)[:, None], x, -np.inf)
@@ -93,4 +93,4 @@ def attention(q, k, v, limit, scale):
     w = p / np.where(z > 0, z, 1)
     with np.errstate(divide="ignore"):
         lse = (np.where(np.isfinite(m), m, 0) + np.log(z))[:, 0]
-    return w @ v, lse, w @ np.abs(v), mag
+    return w @ v, lse, w @ np.abs(v), mag, np.abs(v).sum(0)

@@ -88,14 +88,16 @@ class Problem:
         return R.resa_check_device_status(self.ws, raise_on_error=False)
 
 
-def attention_tolerance(mag, n, a):
-    """Bound on |out - exact| per unit of sum p |v| (a), and on |lse - exact|.
+def attention_tolerance(mag, n, a, vsum=0.0):
+    """Bounds on |out - exact|, with a = sum p |v| and vsum = sum |v|, and on |lse - exact|.
 
     Logits: the products are exact and at most d = 128 of them are added in fp32 in the matrix
     unit, which may drop bits below 2^-22 of the running magnitude at each of 8 steps, and the
     scaling rounds twice more: at most 10 * 2^-22 of sum |q k| = mag.  Weights: e^(2 delta) - 1,
-    2^-21 for the exponential, 2^-21 for the two fp16 halves.  Sums over n weights: one addition
+    2^-21 for the exponential, 2^-21 for the two fp16 halves, whose absolute rounding is half of
+    fp16's smallest step, 2^-25, where the row's largest weight is at least 2^12: 2^-37 of |v|
+    for every key.  Sums over n weights: one addition
     a 16-position step, split over at least 1 warp, 2^-22 each, and 64 more for the merges."""
     delta = 10 * 2.0 ** -22 * mag
     sums = (n / 16 + 64) * 2.0 ** -22
-    return a * (2 * delta + 2.0 ** -20 + 2 * sums) + 1e-30, delta + 2.0 ** -20 + sums
+    return a * (2 * delta + 2.0 ** -20 + 2 * sums) + 2.0 ** -37 * vsum + 1e-30, delta + 2.0 ** -20 + sums

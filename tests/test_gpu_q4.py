@@ -224,8 +224,8 @@ def check_rows(p, out, lse, q, i, h, blocks, limit):
     """Rows out [n, d], lse [n] of queries q [n, d] (float64) over blocks of (sequence i, head h)."""
     k, v, pos = p.keys_values(i, h, blocks)
     lim = np.searchsorted(pos, limit) if blocks is None else np.full(len(q), len(pos))
-    o, z, a, mag = q4.attention(q, k, v, lim, p.d ** -0.5)
-    to, tz = attention_tolerance(mag[:, None], len(pos), a)
+    o, z, a, mag, vsum = q4.attention(q, k, v, lim, p.d ** -0.5)
+    to, tz = attention_tolerance(mag[:, None], len(pos), a, vsum)
     assert (np.abs(out - o) <= to).all(), (i, h, np.abs(out - o).max(), to.min())
     fin = np.isfinite(z)
     assert (np.abs(lse[fin] - z[fin]) <= tz[:, 0][fin] + 2.0 ** -22 * np.abs(z[fin])).all(), (i, h)
