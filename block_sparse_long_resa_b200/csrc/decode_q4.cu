@@ -116,13 +116,18 @@ struct Unit {
     bool live;                 // outputs are written (else they stay as they were)
 };
 
+struct Part {
+    int b, h, rows, ustart, uend;  // rows 0: none
+};
+
 struct DecodeQ4Args {
     Q4Cache c;
     const int32_t *page_table, *seq_len, *n_new, *block_idx, *block_cnt;
     const uint16_t *q;
     float *part_o, *out, *lse;
     float2 *part_ml;
-    uint32_t *tickets, *err;
+    unsigned long long *grid_bar;
+    uint32_t *err;
     RowMap rm;
     int f, max_topk, batch, hq, hkv, g, max_pages, num_pages, bs;
     float scale_log2;
@@ -140,7 +145,8 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     __shared__ int sh_sum[kWarps], sh_unit, sh_first;
     __shared__ int4 sh_units[kThreads];  // (blocks, length, fresh tokens, row) when they fit
     __shared__ float2 sh_ml[kRows];  // a row's maximum and sum
-    __shared__ uint32_t sh_last;
+    __shared__ Part sh_part[2];      // this CTA's partial pieces: the first one, a later one
+    __shared__ uint32_t sh_ok;
 
     pdl_launch_next();
     pdl_wait();
@@ -183,6 +189,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         return x;
     };
 
+    if (tid < 2) sh_part[tid].rows = 0;
     // Prefix sums of the units' blocks: thread t sums units [t * per, ...).
     const int per = (units + kThreads - 1) / kThreads;
     const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
@@ -209,7 +216,9 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     incl += before;
     // CTAs that take work: enough for a step of every warp each
     const int least = max(1, 32 * kWarps / a.bs);
-    const int G = max(1, min((int)gridDim.x, (W + least - 1) / least));
+    int G = max(1, min((int)gridDim.x, (W + least - 1) / least));
+    // With many CTAs a unit, as many for each: equal units then begin with a CTA's share.
+    if (G >= 8 * units) G -= G % units;
     auto entry_of = [&](int q) -> int { return q < G ? (int)((long long)W * q / G) : W; };
     const int x0 = entry_of(cta), x1 = entry_of(cta + 1);
     if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
@@ -226,6 +235,18 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     }
     __syncthreads();
 
+    auto orow_of = [&](int b, int h, int rho) -> size_t {
+        return ((size_t)b * a.f + rho / a.g) * a.hq + (size_t)h * a.g + rho % a.g;
+    };
+    // four places of a row: channels ch, ch + 1 and ch + D/8, ch + D/8 + 1
+    auto store_out = [&](int b, int h, int rho, int p4, float4 v) {
+        float *dst = a.out + orow_of(b, h, rho) * D + (p4 % 4) * (D / 4) + (p4 / 4) * 2;
+        *reinterpret_cast<float2 *>(dst) = make_float2(v.x, v.y);
+        *reinterpret_cast<float2 *>(dst + D / 8) = make_float2(v.z, v.w);
+    };
+    auto lse_of = [&](float ms, float ls) -> float {
+        return ls > 0.f ? (ms - kShift + log2f(ls)) * 0.6931471805599453f : ls == 0.f ? -INFINITY : ls;
+    };
     int u = x0 < x1 ? sh_unit : 0;
     int ustart = x0 < x1 ? sh_first : 0;
     const int sub_shift = a.bs == 64 ? 2 : a.bs == 32 ? 1 : 0;  // tiles a block
@@ -631,21 +652,8 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         __syncthreads();
         const bool whole = j0 == 0 && j1 == un.cnt;
         const float vg = head_scale(a.c.v_scale, h);
-        auto orow_of = [&](int rho) -> size_t {
-            const int qr = rho;
-            return ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
-        };
         // Partial slot of this CTA: 2 cta for its first piece, 2 cta + 1 for a later one.
         const int slot = 2 * cta + (x == x0 ? 0 : 1);
-        // four places of a row: channels ch, ch + 1 and ch + D/8, ch + D/8 + 1
-        auto store_out = [&](int rho, int p4, float4 v) {
-            float *dst = a.out + orow_of(rho) * D + (p4 % 4) * (D / 4) + (p4 / 4) * 2;
-            *reinterpret_cast<float2 *>(dst) = make_float2(v.x, v.y);
-            *reinterpret_cast<float2 *>(dst + D / 8) = make_float2(v.z, v.w);
-        };
-        auto lse_of = [&](float ms, float ls) -> float {
-            return ls > 0.f ? (ms - kShift + log2f(ls)) * 0.6931471805599453f : ls == 0.f ? -INFINITY : ls;
-        };
         for (int e = tid; e < rows_all * (D / 4); e += kThreads) {
             const int rho = e / (D / 4), p4 = e % (D / 4);
             float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -661,107 +669,83 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             const float2 ml = sh_ml[rho];
             if (whole) {
                 const float f2 = ml.y == 0.f ? 0.f : vg / ml.y;
-                store_out(rho, p4, make_float4(os.x * f2, os.y * f2, os.z * f2, os.w * f2));
-                if (a.lse && p4 == 0) a.lse[orow_of(rho)] = lse_of(ml.x, ml.y);
+                store_out(b, h, rho, p4, make_float4(os.x * f2, os.y * f2, os.z * f2, os.w * f2));
+                if (a.lse && p4 == 0) a.lse[orow_of(b, h, rho)] = lse_of(ml.x, ml.y);
             } else {
                 reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * kMaxGroup + rho) * D)[p4] = os;
                 if (p4 == 0) a.part_ml[slot * kMaxGroup + rho] = ml;
             }
         }
-        if (!whole) {
-            __threadfence();
-            __syncthreads();
-            // CTAs q0 .. q1 whose shares meet the unit; only q0's can begin before it
-            const int q0 = (int)((((long long)ustart + 1) * G - 1) / W), q1 = (int)(((long long)uend * G - 1) / W);
-            const int parts = q1 - q0 + 1, odd = entry_of(q0) < ustart ? 1 : 0;
-            if (tid == 0) {
-                const uint32_t k = atomicAdd(&a.tickets[u], 1u);
-                sh_last = k == (uint32_t)(parts - 1);
-                if (sh_last) a.tickets[u] = 0u;
-            }
-            __syncthreads();
-            if (sh_last) {
-                __threadfence();
-                // All parts at once into shared memory (as many as fit), while their
-                // weights are worked out; then four places a thread.
-                float *wt = reinterpret_cast<float *>(smem);  // [rows][parts] weights
-                const int wt_bytes = (rows_all * parts * 4 + 15) & ~15;
-                float *po = reinterpret_cast<float *>(smem + wt_bytes);
-                const int part_floats = rows_all * D;
-                const int cap = (SM::kRing - wt_bytes) / (part_floats * 4);
-                const float *src0 = a.part_o + (size_t)(2 * q0 + odd) * kMaxGroup * D;
-                const float *src = a.part_o + (size_t)(2 * q0) * kMaxGroup * D;
-                const float2 *ml0 = a.part_ml + (2 * q0 + odd) * kMaxGroup, *mls = a.part_ml + 2 * q0 * kMaxGroup;
-                auto fetch = [&](int from) {
-                    for (int q = from + warp; q < min(parts, from + cap); q += kWarps) {
-                        const float *g = q == 0 ? src0 : src + (size_t)q * (2 * kMaxGroup * D);
-                        const uint32_t dst = smem_u32(po + (q - from) * part_floats);
-#pragma unroll 1
-                        for (int i = lane; i < part_floats / 4; i += 32) cp_async16_s(dst + i * 16, g + i * 4);
-                    }
-                    cp_async_commit();
-                };
-                fetch(0);
-                for (int rho = warp; rho < rows_all; rho += kWarps) {
-                    float ms = -INFINITY, ls = 0.f;
-                    for (int q = lane; q < parts; q += 32) {
-                        const float2 ml = __ldcg((q == 0 ? ml0 : mls + q * 2 * kMaxGroup) + rho);
-                        wt[rho * parts + q] = ml.x;
-                        const float mn = fmaxf(ms, ml.x);
-                        ls = mn == -INFINITY ? 0.f : ls * ex2(ms - mn) + ml.y * ex2(ml.x - mn);
-                        ms = mn;
-                    }
-                    float mt = ms;
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o2));
-                    ls = mt == -INFINITY ? 0.f : ls * ex2(ms - mt);
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o2);
-                    const float f3 = ls == 0.f ? 0.f : vg / ls;
-                    for (int q = lane; q < parts; q += 32) {
-                        float &x = wt[rho * parts + q];
-                        x = mt == -INFINITY ? 0.f : ex2(x - mt) * f3;
-                    }
-                    if (a.lse && lane == 0) a.lse[orow_of(rho)] = lse_of(mt, ls);
-                }
-                float4 os[kItems];
-#pragma unroll
-                for (int i = 0; i < kItems; ++i) os[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int from = 0; from < parts; from += cap) {
-                    if (from > 0) {
-                        __syncthreads();
-                        fetch(from);
-                    }
-                    cp_async_wait<0>();
-                    __syncthreads();
-                    const int n = min(cap, parts - from);
-#pragma unroll
-                    for (int i = 0; i < kItems; ++i) {
-                        const int e = tid + i * kThreads;
-                        if (e * 4 < part_floats) {
-                            const float *w = wt + e / (D / 4) * parts + from;
-#pragma unroll 4
-                            for (int q = 0; q < n; ++q) {
-                                const float f2 = w[q];
-                                const float4 v = *reinterpret_cast<const float4 *>(po + q * part_floats + 4 * e);
-                                os[i].x += v.x * f2;
-                                os[i].y += v.y * f2;
-                                os[i].z += v.z * f2;
-                                os[i].w += v.w * f2;
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kItems; ++i) {
-                    const int e = tid + i * kThreads;
-                    if (e * 4 < part_floats) store_out(e / (D / 4), e % (D / 4), os[i]);
-                }
-            }
-        }
+        if (!whole && tid == 0) sh_part[x == x0 ? 0 : 1] = Part{b, h, rows_all, ustart, uend};
         __syncthreads();  // the merge area is the ring again
         x = min(x1, uend);
         ustart = uend;
+    }
+
+    // Merge the units that span CTAs: behind a grid barrier each of a unit's CTAs takes
+    // an equal share of its (row, four channels) items, with gl lanes an item, a lane a part.
+    if (gridDim.x > 1) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) sh_ok = grid_barrier_bounded(a.grid_bar, gridDim.x) ? 1u : 0u;
+        __syncthreads();
+        if (!sh_ok && tid == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+        __threadfence();
+#pragma unroll 1
+        for (int w2 = 0; w2 < 2 && sh_ok; ++w2) {
+            const Part pt = sh_part[w2];
+            if (pt.rows == 0) continue;
+            // CTAs q0 .. q1 whose shares meet the unit; only q0's can begin before it
+            const int q0 = (int)((((long long)pt.ustart + 1) * G - 1) / W);
+            const int q1 = (int)(((long long)pt.uend * G - 1) / W);
+            const int parts = q1 - q0 + 1, odd = entry_of(q0) < pt.ustart ? 1 : 0;
+            const int items = pt.rows * (D / 4);
+            const int i0 = items * (cta - q0) / parts, i1 = items * (cta - q0 + 1) / parts;
+            const int lg = parts > 16 ? 5 : parts > 8 ? 4 : parts > 4 ? 3 : parts > 2 ? 2 : 1;
+            const int gl = 1 << lg, me = tid & (gl - 1);
+            const float vg = head_scale(a.c.v_scale, pt.h);
+#pragma unroll 1
+            for (int base = i0; base < i1; base += kThreads >> lg) {
+                const int e = base + (tid >> lg);
+                const int rho = min(e, i1 - 1) / (D / 4), p4 = min(e, i1 - 1) % (D / 4);
+                float ms = -INFINITY, ls = 0.f;
+                float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int q = me; q < parts; q += gl) {
+                    const size_t at = (size_t)(2 * (q0 + q) + (q == 0 ? odd : 0)) * kMaxGroup + rho;
+                    const float2 ml = __ldcg(a.part_ml + at);
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + p4);
+                    const float mn = fmaxf(ms, ml.x);
+                    const float f1 = mn == -INFINITY ? 0.f : ex2(ms - mn), f2 = mn == -INFINITY ? 0.f : ex2(ml.x - mn);
+                    ms = mn;
+                    ls = ls * f1 + ml.y * f2;
+                    os.x = os.x * f1 + v.x * f2;
+                    os.y = os.y * f1 + v.y * f2;
+                    os.z = os.z * f1 + v.z * f2;
+                    os.w = os.w * f1 + v.w * f2;
+                }
+                float mt = ms;
+                for (int o2 = gl >> 1; o2 > 0; o2 >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o2));
+                const float f1 = mt == -INFINITY ? 0.f : ex2(ms - mt);
+                ls *= f1;
+                os.x *= f1;
+                os.y *= f1;
+                os.z *= f1;
+                os.w *= f1;
+                for (int o2 = gl >> 1; o2 > 0; o2 >>= 1) {
+                    ls += __shfl_xor_sync(0xffffffffu, ls, o2);
+                    os.x += __shfl_xor_sync(0xffffffffu, os.x, o2);
+                    os.y += __shfl_xor_sync(0xffffffffu, os.y, o2);
+                    os.z += __shfl_xor_sync(0xffffffffu, os.z, o2);
+                    os.w += __shfl_xor_sync(0xffffffffu, os.w, o2);
+                }
+                if (me == 0 && e < i1) {
+                    const float f2 = ls == 0.f ? 0.f : vg / ls;
+                    store_out(pt.b, pt.h, rho, p4, make_float4(os.x * f2, os.y * f2, os.z * f2, os.w * f2));
+                    if (a.lse && p4 == 0) a.lse[orow_of(pt.b, pt.h, rho)] = lse_of(mt, ls);
+                }
+            }
+        }
     }
 
     // Units without any block: zeros and -inf, and the errors of every unit.
@@ -783,7 +767,19 @@ cudaError_t launch_t(const DecodeQ4Args &a, int ctas, cudaStream_t st) {
     static std::atomic<int> done[64];
     cudaError_t e = ensure_smem(decode_q4_kernel<D, NT>, smem, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(decode_q4_kernel<D, NT>, dim3(ctas), dim3(32 * SM::kWarps), smem, st, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * SM::kWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
+    attr[1].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, NT>, a);
 }
 
 }  // namespace
@@ -792,7 +788,7 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
                              const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
                              const int32_t *block_idx, const int32_t *block_cnt,
                              int max_topk, int sms, float *part_o, float *part_ml,
-                             uint32_t *tickets, float *out, float *lse, uint32_t *err,
+                             uint32_t *grid_bar, float *out, float *lse, uint32_t *err,
                              cudaStream_t st) {
     DecodeQ4Args a{};
     a.c = c;
@@ -806,7 +802,7 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     a.out = out;
     a.lse = lse;
     a.part_ml = reinterpret_cast<float2 *>(part_ml);
-    a.tickets = tickets;
+    a.grid_bar = reinterpret_cast<unsigned long long *>(grid_bar);
     a.err = err;
     a.rm = s.rows;
     a.f = f;
@@ -819,8 +815,11 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     a.num_pages = s.num_pages;
     a.bs = s.bs;
     a.scale_log2 = s.sm_scale * 1.4426950408889634f;
-    // one CTA per SM; two partial slots a CTA in the decode partials
-    const int ctas = sms < kNumSms ? sms : kNumSms;
+    // one CTA per SM (two partial slots a CTA in the decode partials), no more than the
+    // longest lists could use
+    const long long most = (long long)s.batch * s.hkv * (block_idx ? (long long)max_topk + 1 : s.max_pages);
+    const long long ctas_most = (most * s.bs + 255) / 256;
+    const int all = sms < kNumSms ? sms : kNumSms, ctas = ctas_most < all ? (int)ctas_most : all;
     const int rows = block_idx ? s.g : f * s.g;
     if (s.d == 128) return rows <= 8 ? launch_t<128, 1>(a, ctas, st) : launch_t<128, 2>(a, ctas, st);
     return rows <= 8 ? launch_t<64, 1>(a, ctas, st) : launch_t<64, 2>(a, ctas, st);

@@ -153,7 +153,7 @@ resa_status_t resa_sparse_decode_q4(const resa_config_t *cfg, const resa_cache_q
     return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, 1, nullptr,
                                         block_idx, block_cnt, max_topk, sm_count(),
                                         at<float>(ws, w.dec_o), at<float>(ws, w.dec_lse),
-                                        at<uint32_t>(ws, w.dec_ticket), out, lse_opt,
+                                        at<uint32_t>(ws, w.err + kDecBarrierOffset), out, lse_opt,
                                         at<uint32_t>(ws, w.err), stream));
 }
 
@@ -178,7 +178,7 @@ resa_status_t resa_attention_q4(const resa_config_t *cfg, const resa_cache_q4_t 
     if (f * s.g <= kMaxGroup)
         return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
                                             nullptr, nullptr, 0, sm_count(), at<float>(ws, w.dec_o),
-                                            at<float>(ws, w.dec_lse), at<uint32_t>(ws, w.dec_ticket),
+                                            at<float>(ws, w.dec_lse), at<uint32_t>(ws, w.err + kDecBarrierOffset),
                                             out, lse_opt, err, stream));
     return cuda_status(launch_chunk_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
                                        sm_count(), at<float>(ws, w.rect_o), at<float>(ws, w.rect_lse),

@@ -131,7 +131,7 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
                              const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
                              const int32_t *block_idx, const int32_t *block_cnt,
                              int max_topk, int sms, float *part_o, float *part_ml,
-                             uint32_t *tickets, float *out, float *lse, uint32_t *err,
+                             uint32_t *grid_bar, float *out, float *lse, uint32_t *err,
                              cudaStream_t st);
 // The same for chunks of more than kMaxGroup rows, on tcgen05 (part_o and part_ml: two row
 // groups a CTA; grid_bar: a 64-bit barrier word).
