@@ -5,12 +5,11 @@
 //
 // Grid (CTAs of keys and values, then CTAs of queries; batch).  A key CTA owns
 // one block of the cache that holds fresh tokens and a range of kv heads, so it
-// alone writes that block's slots and its descriptor: 16 tokens at a time it
-// brings the keys as stored (rotated, or read back from the cache below the
-// first fresh slot) into shared memory and folds their min / max per channel.
-// A query CTA rotates up to kQueryTokens tokens of every query head.  The
-// angles of a CTA's tokens are worked out once, in a shared table, and used by
-// all its heads.
+// alone writes that block's slots and its descriptor: its warps take a token
+// each, bring the keys as stored (rotated, or read back from the cache below the
+// first fresh slot) into shared memory, and the CTA folds their min / max per
+// channel.  Of a query CTA a warp, or several where there are few tokens, takes a
+// token.  A warp works out its token's angles once, for all heads.
 //
 // An angle is pos * inv_freq in turns in fp64, reduced to [-1/2, 1/2] before
 // the sine, so that a position of 2^20 has as good an angle as position 1.  Keys
@@ -22,13 +21,16 @@ namespace resa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kQueryTokens = 16;  // tokens a query CTA rotates
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeyRows = 256;  // most (token, head) rows of keys a CTA holds, D channels each
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 struct AppendGeom {
-    int hq, hkv, heads;  // heads: kv heads a key CTA takes
+    int hq, hkv, lg_heads;  // 2^lg_heads kv heads a key CTA takes
     int max_pages, num_pages, bs;
     int key_ctas;        // CTAs of keys and values along x
+    int q_tokens;        // tokens a query CTA takes: 1, 2, 4 or 8
+    int tab;             // byte offset of the angles in shared memory
     RowMap rm;
 };
 
@@ -76,40 +78,33 @@ __device__ __forceinline__ void fold2(uint32_t &mn, uint32_t &mx, uint32_t x) {
          (bf_hi(x) > bf_hi(mx) ? x & 0xffff0000u : mx & 0xffff0000u);
 }
 
-// Work items of one head row of D channels: rotated items first (a pair of
-// 16-byte vectors half a rotation apart, or one vector of adjacent pairs), then
-// the vectors that are copied.
-template <int D>
-struct RowItems {
-    int rotated, all;
-    __device__ __forceinline__ RowItems(int rot, int interleaved)
-        : rotated(interleaved ? rot / 8 : rot / 16), all(rotated + (D - rot) / 8) {}
-};
-
-// Apply item `it` of a row: src and dst in 16-byte vectors of the row.
-template <int D, typename T, typename T2>
-__device__ __forceinline__ void rotate_item(const uint4 *src, uint4 *dst, uint4 *dst2, int it,
-                                            const RowItems<D> &ri, int rot, int interleaved,
+// A head row of D channels is D / 16 slots of two 16-byte vectors each: a pair of
+// vectors half a rotation apart, two vectors of adjacent pairs, or two that are
+// copied.  The vectors of slot it:
+__device__ __forceinline__ void slot_vectors(int it, int rot, int interleaved, int &c1, int &c2) {
+    const bool apart = it < rot / 16 && !interleaved;
+    c1 = apart ? it : 2 * it;
+    c2 = apart ? it + rot / 16 : 2 * it + 1;
+}
+// Rotate them; cs: (cos, sin) of the token's frequencies.
+template <typename T, typename T2>
+__device__ __forceinline__ void rotate_slot(uint4 &x1, uint4 &x2, int it, int rot, int interleaved,
                                             const T2 *cs) {
-    if (it >= ri.rotated) {
-        const int c = rot / 8 + it - ri.rotated;
-        const uint4 x = src[c];
-        dst[c] = x;
-        if (dst2) dst2[c] = x;
-    } else if (interleaved) {
-        uint4 x = src[it];
-        rotate4_adjacent<T>(x, cs + 4 * it);
-        dst[it] = x;
-        if (dst2) dst2[it] = x;
+    if (it >= rot / 16) return;
+    if (interleaved) {
+        rotate4_adjacent<T>(x1, cs + 8 * it);
+        rotate4_adjacent<T>(x2, cs + 8 * it + 4);
     } else {
-        uint4 x1 = src[it], x2 = src[it + rot / 16];
         rotate8<T>(x1, x2, cs + 8 * it);
-        dst[it] = x1;
-        dst[it + rot / 16] = x2;
-        if (dst2) {
-            dst2[it] = x1;
-            dst2[it + rot / 16] = x2;
-        }
+    }
+}
+
+__device__ __forceinline__ void unpack16(const uint4 &x0, const uint4 &x1, float (&x)[kQ4Group]) {
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[2 * i] = bf_lo(w[i]);
+        x[2 * i + 1] = bf_hi(w[i]);
     }
 }
 
@@ -117,10 +112,12 @@ template <int D, bool Q4>
 __global__ void __launch_bounds__(kThreads)
     append_rope_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ AppendGeom gm,
                        uint32_t *err) {
-    constexpr int CPR = D / 8;  // 16-byte vectors a row
+    constexpr int CPR = D / 8;     // 16-byte vectors a row
+    constexpr int SPR = D / 16;    // slots a row, and groups of 16 channels
     extern __shared__ __align__(16) uint8_t smem[];
+    pdl_launch_next();
     pdl_wait();
-    const int b = blockIdx.y, tid = threadIdx.x;
+    const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool first = blockIdx.x == 0 && tid == 0;
     const int n = a.n_new ? a.n_new[b] : a.f;
     if (n == 0) return;
@@ -136,181 +133,172 @@ __global__ void __launch_bounds__(kThreads)
     }
     const int start = L - n;  // cache position of the first fresh token
     const int half = a.rot / 2;
-    const RowItems<D> ri(a.rot, a.interleaved);
 
     if ((int)blockIdx.x >= gm.key_ctas) {  // ------------------------------- queries
-        const int r0 = ((int)blockIdx.x - gm.key_ctas) * kQueryTokens;
-        const int nt = min(kQueryTokens, n - r0);
-        if (nt <= 0) return;
-        float2 *tab = reinterpret_cast<float2 *>(smem);  // [kQueryTokens][half]
-        for (int e = tid; e < nt * half; e += kThreads) {
-            const int t = e / half, i = e - t * half;
+        // warps per token: 8 / q_tokens, each a share of the heads' slots
+        const int wpt = kWarps / gm.q_tokens;
+        const int r = ((int)blockIdx.x - gm.key_ctas) * gm.q_tokens + warp / wpt;
+        if (r >= n) return;
+        float2 *tab = reinterpret_cast<float2 *>(smem) + warp * (D / 2);
+        for (int i = lane; i < half; i += 32) {
             float s, c;
-            sincospif(2.f * (float)turns(a, b, r0 + t, start + r0 + t, i), &s, &c);
+            sincospif(2.f * (float)turns(a, b, r, start + r, i), &s, &c);
             const float m = (float)a.mscale;
-            tab[t * half + i] = make_float2(c * m, s * m);
+            tab[i] = make_float2(c * m, s * m);
         }
-        __syncthreads();
-        const uint16_t *q = static_cast<const uint16_t *>(a.q);
-        uint16_t *qo = static_cast<uint16_t *>(a.q_out);
-        for (int e = tid; e < nt * gm.hq * ri.all; e += kThreads) {
-            const int th = e / ri.all, it = e - th * ri.all;
-            const int t = th / gm.hq, h = th - t * gm.hq;
-            const size_t tok = (size_t)b * a.f + r0 + t;
-            rotate_item<D, float>(
-                reinterpret_cast<const uint4 *>(q + tok * a.q_stride + (size_t)h * D),
-                reinterpret_cast<uint4 *>(qo + (tok * gm.hq + h) * D), nullptr, it, ri, a.rot,
-                a.interleaved, tab + t * half);
+        __syncwarp();
+        const size_t tok = (size_t)b * a.f + r;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + tok * a.q_stride);
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) + tok * gm.hq * D);
+        const int slots = gm.hq * SPR, step = 32 * wpt;
+        constexpr int kAhead = 4;
+        for (int e0 = (warp % wpt) * 32 + lane; e0 < slots; e0 += kAhead * step) {
+            uint4 x1[kAhead], x2[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int e = e0 + k * step;
+                if (e < slots) {
+                    int c1, c2;
+                    slot_vectors(e % SPR, a.rot, a.interleaved, c1, c2);
+                    x1[k] = src[e / SPR * CPR + c1];
+                    x2[k] = src[e / SPR * CPR + c2];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int e = e0 + k * step;
+                if (e < slots) {
+                    int c1, c2;
+                    slot_vectors(e % SPR, a.rot, a.interleaved, c1, c2);
+                    rotate_slot<float>(x1[k], x2[k], e % SPR, a.rot, a.interleaved, tab);
+                    dst[e / SPR * CPR + c1] = x1[k];
+                    dst[e / SPR * CPR + c2] = x2[k];
+                }
+            }
         }
         return;
     }
 
     // ------------------------------------------------------------ keys and values
-    const int groups = gm.hkv / gm.heads;
+    const int heads = 1 << gm.lg_heads, groups = gm.hkv >> gm.lg_heads;
     const int blk = start / gm.bs + (int)blockIdx.x / groups;
-    const int h0 = ((int)blockIdx.x % groups) * gm.heads;
+    const int h0 = ((int)blockIdx.x % groups) * heads;
     if (blk > (L - 1) / gm.bs) return;
     const int page = a.page_table[(size_t)row * gm.max_pages + blk];
     if (page < 0 || page >= gm.num_pages) {
         if (tid == 0) set_error(err, RESA_DEVERR_PAGE);
         return;
     }
-    double2 *tab = reinterpret_cast<double2 *>(smem);                       // [16][half]
-    uint4 *keys = reinterpret_cast<uint4 *>(smem + kTileRows * half * 16);  // [16][heads][CPR]
-    const int valid = min(gm.bs, L - blk * gm.bs);  // slots of the block below seq_len
+    uint4 *keys = reinterpret_cast<uint4 *>(smem);  // [token][head][CPR]
     const int pos0 = blk * gm.bs;
-    const size_t prow = (size_t)page * gm.hkv;  // (page, head) row base
-    constexpr int kFold = kMaxKvHeads * (D / 2) / kThreads;  // channel pairs a thread folds
-    uint32_t mn[kFold], mx[kFold];  // bf16 pairs
-#pragma unroll
-    for (int j = 0; j < kFold; ++j) mn[j] = mx[j] = 0u;
+    const int valid = min(gm.bs, L - pos0);                    // slots of the block below seq_len
+    const int fresh0 = max(0, start - pos0);                   // the first fresh one
+    const int r0 = pos0 + fresh0 - start;                      // its row in the call's arrays
+    const int nf = valid - fresh0;
+    const size_t prow = (size_t)page * gm.hkv + h0;            // (page, head) row base
     bool bad = false;
 
-    for (int t0 = 0; t0 < valid; t0 += kTileRows) {
-        const int nt = min(kTileRows, valid - t0);
-        const int fresh0 = max(0, min(nt, start - pos0 - t0));  // first fresh slot of these
-        const int nf = nt - fresh0;
-        const int r0 = pos0 + t0 + fresh0 - start;  // its row in the call's arrays
-        if (t0) __syncthreads();
-        for (int e = tid; e < nf * half; e += kThreads) {
-            const int t = e / half, i = e - t * half;
+    // keys below the first fresh slot, as stored
+    for (int e = tid; e < fresh0 * heads * CPR; e += kThreads) {
+        const int c = e % CPR, th = e / CPR;
+        const int h = th & (heads - 1), t = th >> gm.lg_heads;
+        const size_t slot = (prow + h) * gm.bs + t;
+        if (Q4) {
+            const uint32_t w = static_cast<const uint32_t *>(a.k)[slot * CPR + c];
+            const uint32_t sf = static_cast<const uint8_t *>(a.k_sf)[slot * SPR + c / 2];
+            keys[e] = q4_values_bf16(w, sf, head_scale(a.k_scale, h0 + h));
+        } else {
+            keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
+        }
+    }
+    // fresh keys, rotated, into shared memory (and the bf16 cache): a warp a token
+    double2 *tab = reinterpret_cast<double2 *>(smem + gm.tab) + warp * (D / 2);
+    for (int t = warp; t < nf; t += kWarps) {
+        __syncwarp();
+        for (int i = lane; i < half; i += 32) {
             double s, c;
             sincospi(2.0 * turns(a, b, r0 + t, start + r0 + t, i), &s, &c);
-            tab[t * half + i] = make_double2(c * a.mscale, s * a.mscale);
+            tab[i] = make_double2(c * a.mscale, s * a.mscale);
         }
-        // keys below the first fresh slot, as stored
-        for (int e = tid; e < fresh0 * gm.heads * CPR; e += kThreads) {
-            const int th = e / CPR, c = e - th * CPR;
-            const int t = th / gm.heads, h = th - t * gm.heads;
-            const size_t slot = (prow + h0 + h) * gm.bs + t0 + t;
-            if (Q4) {
-                const uint32_t w = static_cast<const uint32_t *>(a.k)[slot * CPR + c];
-                const uint32_t sf = static_cast<const uint8_t *>(a.k_sf)[slot * (D / 16) + c / 2];
-                keys[e] = q4_values_bf16(w, sf, head_scale(a.k_scale, h0 + h));
-            } else {
-                keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
-            }
-        }
-        // values
-        if (Q4) {
-            for (int e = tid; e < nf * gm.heads * (D / 16); e += kThreads) {
-                const int th = e / (D / 16), gi = e - th * (D / 16);
-                const int t = th / gm.heads, h = th - t * gm.heads;
-                const size_t tok = (size_t)b * a.f + r0 + t;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const uint16_t *>(a.vn) + tok * a.v_stride + (size_t)(h0 + h) * D +
-                    gi * 16);
-                const uint4 x0 = src[0], x1 = src[1];
-                const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                float x[kQ4Group];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[2 * i] = bf_lo(w[i]);
-                    x[2 * i + 1] = bf_hi(w[i]);
-                }
-                uint2 codes;
-                uint32_t sf;
-                bad |= q4_quantise(x, 1.f / head_scale(a.v_scale, h0 + h), codes, sf);
-                const size_t slot = (prow + h0 + h) * gm.bs + t0 + fresh0 + t;
-                static_cast<uint2 *>(a.v)[slot * (D / 16) + gi] = codes;
-                static_cast<uint8_t *>(a.v_sf)[slot * (D / 16) + gi] = (uint8_t)sf;
-            }
-        } else {
-            for (int e = tid; e < nf * gm.heads * CPR; e += kThreads) {
-                const int th = e / CPR, c = e - th * CPR;
-                const int t = th / gm.heads, h = th - t * gm.heads;
-                const size_t tok = (size_t)b * a.f + r0 + t;
-                const size_t slot = (prow + h0 + h) * gm.bs + t0 + fresh0 + t;
-                static_cast<uint4 *>(a.v)[slot * CPR + c] = reinterpret_cast<const uint4 *>(
-                    static_cast<const uint16_t *>(a.vn) + tok * a.v_stride + (size_t)(h0 + h) * D)[c];
-            }
-        }
-        __syncthreads();
-        // fresh keys, rotated, into shared memory (and the bf16 cache)
-        for (int e = tid; e < nf * gm.heads * ri.all; e += kThreads) {
-            const int th = e / ri.all, it = e - th * ri.all;
-            const int t = th / gm.heads, h = th - t * gm.heads;
-            const size_t tok = (size_t)b * a.f + r0 + t;
-            const size_t slot = (prow + h0 + h) * gm.bs + t0 + fresh0 + t;
-            rotate_item<D, double>(
-                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) +
-                                                tok * a.k_stride + (size_t)(h0 + h) * D),
-                keys + ((fresh0 + t) * gm.heads + h) * CPR,
-                Q4 ? nullptr : static_cast<uint4 *>(a.k) + slot * CPR, it, ri, a.rot, a.interleaved,
-                tab + t * half);
-        }
-        __syncthreads();
-        if (Q4) {
-            // 4-bit codes of the fresh keys; shared memory then holds what they stand for
-            for (int e = tid; e < nf * gm.heads * (D / 16); e += kThreads) {
-                const int th = e / (D / 16), gi = e - th * (D / 16);
-                const int t = th / gm.heads, h = th - t * gm.heads;
-                uint4 *kp = keys + ((fresh0 + t) * gm.heads + h) * CPR + 2 * gi;
-                const uint32_t w[8] = {kp[0].x, kp[0].y, kp[0].z, kp[0].w,
-                                       kp[1].x, kp[1].y, kp[1].z, kp[1].w};
-                float x[kQ4Group];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[2 * i] = bf_lo(w[i]);
-                    x[2 * i + 1] = bf_hi(w[i]);
-                }
-                const float g = head_scale(a.k_scale, h0 + h);
-                uint2 codes;
-                uint32_t sf;
-                bad |= q4_quantise(x, 1.f / g, codes, sf);
-                const size_t slot = (prow + h0 + h) * gm.bs + t0 + fresh0 + t;
-                static_cast<uint2 *>(a.k)[slot * (D / 16) + gi] = codes;
-                static_cast<uint8_t *>(a.k_sf)[slot * (D / 16) + gi] = (uint8_t)sf;
-                kp[0] = q4_values_bf16(codes.x, sf, g);
-                kp[1] = q4_values_bf16(codes.y, sf, g);
-            }
-            __syncthreads();
-        }
-        const uint32_t *kw = reinterpret_cast<const uint32_t *>(keys);
-#pragma unroll
-        for (int j = 0; j < kFold; ++j) {
-            const int e = tid + j * kThreads;  // (head, channel pair)
-            if (e < gm.heads * (D / 2)) {
-                for (int t = 0; t < nt; ++t) {
-                    const uint32_t w = kw[t * gm.heads * (D / 2) + e];
-                    if (t0 + t == 0)
-                        mn[j] = mx[j] = w;
-                    else
-                        fold2(mn[j], mx[j], w);
-                }
+        __syncwarp();
+        const size_t tok = (size_t)b * a.f + r0 + t;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) + tok * a.k_stride +
+                                                           (size_t)h0 * D);
+        uint4 *dst = keys + (fresh0 + t) * heads * CPR;
+#pragma unroll 2
+        for (int e = lane; e < heads * SPR; e += 32) {
+            const int it = e % SPR, h = e / SPR;
+            int c1, c2;
+            slot_vectors(it, a.rot, a.interleaved, c1, c2);
+            uint4 x1 = src[h * CPR + c1], x2 = src[h * CPR + c2];
+            rotate_slot<double>(x1, x2, it, a.rot, a.interleaved, tab);
+            dst[h * CPR + c1] = x1;
+            dst[h * CPR + c2] = x2;
+            if (!Q4) {
+                uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + fresh0 + t) * CPR;
+                out[c1] = x1;
+                out[c2] = x2;
             }
         }
     }
-    uint32_t *desc = static_cast<uint32_t *>(a.desc);
-#pragma unroll
-    for (int j = 0; j < kFold; ++j) {
-        const int e = tid + j * kThreads;
-        if (e < gm.heads * (D / 2)) {
-            const int h = e / (D / 2), c = e - h * (D / 2);
-            uint32_t *d = desc + (prow + h0 + h) * D + c;  // [2][D / 2] words a (page, head)
-            d[0] = mn[j];
-            d[D / 2] = mx[j];
+    // values
+    if (Q4) {
+        for (int e = tid; e < nf * heads * SPR; e += kThreads) {
+            const int gi = e % SPR, th = e / SPR;
+            const int h = th & (heads - 1), t = th >> gm.lg_heads;
+            const size_t tok = (size_t)b * a.f + r0 + t;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const uint16_t *>(a.vn) + tok * a.v_stride + (size_t)(h0 + h) * D + gi * 16);
+            float x[kQ4Group];
+            unpack16(src[0], src[1], x);
+            uint2 codes;
+            uint32_t sf;
+            bad |= q4_quantise(x, 1.f / head_scale(a.v_scale, h0 + h), codes, sf);
+            const size_t slot = (prow + h) * gm.bs + fresh0 + t;
+            static_cast<uint2 *>(a.v)[slot * SPR + gi] = codes;
+            static_cast<uint8_t *>(a.v_sf)[slot * SPR + gi] = (uint8_t)sf;
         }
+    } else {
+#pragma unroll 4
+        for (int e = tid; e < nf * heads * CPR; e += kThreads) {
+            const int c = e % CPR, th = e / CPR;
+            const int h = th & (heads - 1), t = th >> gm.lg_heads;
+            const size_t tok = (size_t)b * a.f + r0 + t;
+            static_cast<uint4 *>(a.v)[((prow + h) * gm.bs + fresh0 + t) * CPR + c] = reinterpret_cast<const uint4 *>(
+                static_cast<const uint16_t *>(a.vn) + tok * a.v_stride + (size_t)(h0 + h) * D)[c];
+        }
+    }
+    __syncthreads();
+    if (Q4) {
+        // 4-bit codes of the fresh keys; shared memory then holds what they stand for
+        for (int e = tid; e < nf * heads * SPR; e += kThreads) {
+            const int gi = e % SPR, th = e / SPR;
+            const int h = th & (heads - 1), t = th >> gm.lg_heads;
+            uint4 *kp = keys + ((fresh0 + t) * heads + h) * CPR + 2 * gi;
+            float x[kQ4Group];
+            unpack16(kp[0], kp[1], x);
+            const float g = head_scale(a.k_scale, h0 + h);
+            uint2 codes;
+            uint32_t sf;
+            bad |= q4_quantise(x, 1.f / g, codes, sf);
+            const size_t slot = (prow + h) * gm.bs + fresh0 + t;
+            static_cast<uint2 *>(a.k)[slot * SPR + gi] = codes;
+            static_cast<uint8_t *>(a.k_sf)[slot * SPR + gi] = (uint8_t)sf;
+            kp[0] = q4_values_bf16(codes.x, sf, g);
+            kp[1] = q4_values_bf16(codes.y, sf, g);
+        }
+        __syncthreads();
+    }
+    // descriptors: a thread two channels of a head
+    const uint32_t *kw = reinterpret_cast<const uint32_t *>(keys);
+    const int width = heads * (D / 2);
+    for (int e = tid; e < width; e += kThreads) {
+        uint32_t mn = kw[e], mx = mn;
+#pragma unroll 4
+        for (int t = 1; t < valid; ++t) fold2(mn, mx, kw[t * width + e]);
+        uint32_t *d = static_cast<uint32_t *>(a.desc) + (prow + e / (D / 2)) * D + e % (D / 2);  // [2][D / 2] words
+        d[0] = mn;
+        d[D / 2] = mx;
     }
     if (Q4 && bad) set_error(err, RESA_DEVERR_NONFINITE);
 }
@@ -320,44 +308,83 @@ __global__ void __launch_bounds__(kThreads)
 // ---------------------------------------------------------------------------
 constexpr int kExpandTokens = 64;  // positions a CTA expands
 
-// Grid (ceil(max positions / kExpandTokens), batch).  A thread turns eight
-// channels (4 bytes of codes) into one 16-byte vector, so reads and writes of a
-// warp are contiguous runs.
+// Grid (ceil(max positions / kExpandTokens), batch).  A thread turns a group of 16
+// channels (8 bytes of codes and a scale) into one 32-byte store, kAhead groups in
+// flight; a warp's reads and writes are contiguous runs.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-    expand_q4_kernel(const Q4Cache c, const int32_t *__restrict__ page_table,
-                     const int32_t *__restrict__ seq_len, uint4 *__restrict__ k_out,
-                     uint4 *__restrict__ v_out, int hkv, int max_pages, int num_pages, int bs,
-                     const RowMap rm, uint32_t *err) {
-    constexpr int CPR = D / 8;
+    expand_q4_kernel(const __grid_constant__ Q4Cache c, const int32_t *__restrict__ page_table,
+                     const int32_t *__restrict__ seq_len, uint16_t *__restrict__ k_out,
+                     uint16_t *__restrict__ v_out, int lg_hkv, int max_pages, int num_pages, int lg_bs,
+                     const RowMap rm, bool wide, uint32_t *err) {
+    constexpr int kAhead = 4, LG = D == 128 ? 3 : 2;  // 2^LG groups a row
+    __shared__ int pages[kExpandTokens / 16];
+    pdl_launch_next();
     pdl_wait();
     const int b = blockIdx.y, tid = threadIdx.x;
     const bool first = blockIdx.x == 0 && tid == 0;
     const int row = cache_row(rm, b, first ? err : nullptr);
     const int L = row_seq_len(seq_len, row);
-    if (L < 0 || (long long)L > (long long)max_pages * bs || row < 0) {
+    if (L < 0 || (long long)L > ((long long)max_pages << lg_bs) || row < 0) {
         if (first) set_error(err, RESA_DEVERR_SEQ_LEN);
         return;
     }
     const long long p0 = (long long)blockIdx.x * kExpandTokens;
-    const int per_page = hkv * bs * CPR;
-    for (long long p = p0; p < p0 + kExpandTokens && p < L; p += bs) {
-        const int blk = (int)(p / bs), valid = min(bs, L - (int)p);
-        const int page = page_table[(size_t)row * max_pages + blk];
+    if (p0 >= L) return;
+    const int left = min(kExpandTokens, L - (int)p0);  // positions of this CTA
+    const int np = (left + (1 << lg_bs) - 1) >> lg_bs;  // pages of this CTA
+    if (tid < np) {
+        int page = page_table[(size_t)row * max_pages + (int)(p0 >> lg_bs) + tid];
         if (page < 0 || page >= num_pages) {
-            if (tid == 0) set_error(err, RESA_DEVERR_PAGE);
-            continue;
+            set_error(err, RESA_DEVERR_PAGE);
+            page = -1;
         }
-        const size_t base = (size_t)page * per_page;
-        for (int e = tid; e < 2 * per_page; e += kThreads) {
-            const bool is_v = e >= per_page;
-            const int i = is_v ? e - per_page : e;
-            const int hs = i / CPR, h = hs / bs, t = hs - h * bs;
-            if (t >= valid) continue;
-            const uint32_t w = reinterpret_cast<const uint32_t *>(is_v ? c.v : c.k)[base + i];
-            const uint32_t sf = (is_v ? c.v_sf : c.k_sf)[(base + i) / 2];
-            const float g = head_scale(is_v ? c.v_scale : c.k_scale, h);
-            (is_v ? v_out : k_out)[base + i] = q4_values_bf16(w, sf, g);
+        pages[tid] = page;
+    }
+    __syncthreads();
+    const int lg_page = lg_hkv + lg_bs + LG;  // groups of a page, of K or V
+    const int all = np << (lg_page + 1);
+    // group e: its place in the cache, or false where there is none
+    auto place = [&](int e, size_t &at, bool &is_v, int &h) -> bool {
+        const int pi = e >> (lg_page + 1), i = e & ((1 << lg_page) - 1);
+        const int t = (i >> LG) & ((1 << lg_bs) - 1);
+        is_v = (e >> lg_page) & 1;
+        h = i >> (LG + lg_bs);
+        if (e >= all || (pi << lg_bs) + t >= left || pages[pi] < 0) return false;
+        at = ((size_t)pages[pi] << lg_page) + i;
+        return true;
+    };
+    for (int e0 = tid; e0 < all; e0 += kAhead * kThreads) {
+        uint2 w[kAhead];
+        uint32_t sf[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            size_t at;
+            bool is_v;
+            int h;
+            if (place(e0 + k * kThreads, at, is_v, h)) {
+                w[k] = __ldcs(reinterpret_cast<const uint2 *>(is_v ? c.v : c.k) + at);
+                sf[k] = (is_v ? c.v_sf : c.k_sf)[at];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            size_t at;
+            bool is_v;
+            int h;
+            if (place(e0 + k * kThreads, at, is_v, h)) {
+                const float g = head_scale(is_v ? c.v_scale : c.k_scale, h);
+                const uint4 x = q4_values_bf16(w[k].x, sf[k], g), y = q4_values_bf16(w[k].y, sf[k], g);
+                uint16_t *dst = (is_v ? v_out : k_out) + at * 16;
+                if (wide) {
+                    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x.x),
+                                 "r"(x.y), "r"(x.z), "r"(x.w), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                                 : "memory");
+                } else {  // pages aligned to 16 bytes only
+                    reinterpret_cast<uint4 *>(dst)[0] = x;
+                    reinterpret_cast<uint4 *>(dst)[1] = y;
+                }
+            }
         }
     }
 }
@@ -367,18 +394,23 @@ cudaError_t launch_append_t(const Shape &s, const AppendArgs &a, uint32_t *err, 
     AppendGeom gm{};
     gm.hq = s.hq;
     gm.hkv = s.hkv;
-    gm.heads = s.hkv;
+    const int heads = s.hkv < kKeyRows / s.bs ? s.hkv : kKeyRows / s.bs;
+    gm.lg_heads = heads == 8 ? 3 : heads == 4 ? 2 : heads == 2 ? 1 : 0;
+    gm.tab = s.bs * heads * D * 2;
     gm.max_pages = s.max_pages;
     gm.num_pages = s.num_pages;
     gm.bs = s.bs;
     gm.rm = s.rows;
-    const int blocks = a.f / s.bs + 2;  // blocks f tokens can touch
-    gm.key_ctas = (blocks < s.max_pages ? blocks : s.max_pages) * (s.hkv / gm.heads);
-    const int query_ctas = a.q ? (a.f - 1) / kQueryTokens + 1 : 0;
-    const size_t keys = (size_t)kTileRows * (a.rot / 2) * 16 + (size_t)kTileRows * gm.heads * D * 2;
-    const size_t queries = (size_t)kQueryTokens * (a.rot / 2) * 8;
+    const int blocks = (int)(((long long)a.f + s.bs - 2) / s.bs + 1);  // blocks f tokens can touch
+    gm.key_ctas = (blocks < s.max_pages ? blocks : s.max_pages) * (s.hkv / heads);
+    gm.q_tokens = a.f >= kWarps ? kWarps : a.f >= 4 ? 4 : a.f >= 2 ? 2 : 1;
+    const int query_ctas = a.q ? (a.f - 1) / gm.q_tokens + 1 : 0;
+    constexpr int most = kKeyRows * D * 2 + kWarps * (D / 2) * 16;
+    static std::atomic<int> done[64];
+    cudaError_t e = ensure_smem(append_rope_kernel<D, Q4>, most, done);
+    if (e != cudaSuccess) return e;
     return launch_pdl(append_rope_kernel<D, Q4>, dim3(gm.key_ctas + query_ctas, s.batch),
-                      dim3(kThreads), keys > queries ? keys : queries, st, a, gm, err);
+                      dim3(kThreads), gm.tab + kWarps * (D / 2) * 16, st, a, gm, err);
 }
 
 }  // namespace
@@ -397,8 +429,10 @@ cudaError_t launch_expand_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     const dim3 grid((unsigned)(((long long)s.max_pages * s.bs + kExpandTokens - 1) / kExpandTokens),
                     s.batch);
     auto kernel = s.d == 128 ? expand_q4_kernel<128> : expand_q4_kernel<64>;
-    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, c, page_table, seq_len, (uint4 *)k_out,
-                      (uint4 *)v_out, s.hkv, s.max_pages, s.num_pages, s.bs, s.rows, err);
+    const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
+    auto lg = [](int x) { return x == 1 ? 0 : x == 2 ? 1 : x == 4 ? 2 : x == 8 ? 3 : x == 16 ? 4 : x == 32 ? 5 : 6; };
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, c, page_table, seq_len, (uint16_t *)k_out,
+                      (uint16_t *)v_out, lg(s.hkv), s.max_pages, s.num_pages, lg(s.bs), s.rows, wide, err);
 }
 
 }  // namespace resa
