@@ -86,16 +86,16 @@ __device__ __forceinline__ void slot_vectors(int it, int rot, int interleaved, i
     c1 = apart ? it : 2 * it;
     c2 = apart ? it + rot / 16 : 2 * it + 1;
 }
-// Rotate them; cs: (cos, sin) of the token's frequencies.
+// Rotate them; cs: (cos, sin) of the slot's eight frequencies.
 template <typename T, typename T2>
 __device__ __forceinline__ void rotate_slot(uint4 &x1, uint4 &x2, int it, int rot, int interleaved,
-                                            const T2 *cs) {
+                                            const T2 (&cs)[8]) {
     if (it >= rot / 16) return;
     if (interleaved) {
-        rotate4_adjacent<T>(x1, cs + 8 * it);
-        rotate4_adjacent<T>(x2, cs + 8 * it + 4);
+        rotate4_adjacent<T>(x1, cs);
+        rotate4_adjacent<T>(x2, cs + 4);
     } else {
-        rotate8<T>(x1, x2, cs + 8 * it);
+        rotate8<T>(x1, x2, cs);
     }
 }
 
@@ -151,6 +151,14 @@ __global__ void __launch_bounds__(kThreads)
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + tok * a.q_stride);
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) + tok * gm.hq * D);
         const int slots = gm.hq * SPR, step = 32 * wpt;
+        // a lane's slots are all slot `it` of a head: its angles stay in registers (read from
+        // shared memory for each head they took most of the time)
+        const int it = lane % SPR;
+        int c1, c2;
+        slot_vectors(it, a.rot, a.interleaved, c1, c2);
+        float2 cs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = tab[8 * it + i];
         constexpr int kAhead = 4;
         for (int e0 = (warp % wpt) * 32 + lane; e0 < slots; e0 += kAhead * step) {
             uint4 x1[kAhead], x2[kAhead];
@@ -158,8 +166,6 @@ __global__ void __launch_bounds__(kThreads)
             for (int k = 0; k < kAhead; ++k) {
                 const int e = e0 + k * step;
                 if (e < slots) {
-                    int c1, c2;
-                    slot_vectors(e % SPR, a.rot, a.interleaved, c1, c2);
                     x1[k] = src[e / SPR * CPR + c1];
                     x2[k] = src[e / SPR * CPR + c2];
                 }
@@ -168,9 +174,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int k = 0; k < kAhead; ++k) {
                 const int e = e0 + k * step;
                 if (e < slots) {
-                    int c1, c2;
-                    slot_vectors(e % SPR, a.rot, a.interleaved, c1, c2);
-                    rotate_slot<float>(x1[k], x2[k], e % SPR, a.rot, a.interleaved, tab);
+                    rotate_slot<float>(x1[k], x2[k], it, a.rot, a.interleaved, cs);
                     dst[e / SPR * CPR + c1] = x1[k];
                     dst[e / SPR * CPR + c2] = x2[k];
                 }
@@ -213,6 +217,9 @@ __global__ void __launch_bounds__(kThreads)
     }
     // fresh keys, rotated, into shared memory (and the bf16 cache): a warp a token
     double2 *tab = reinterpret_cast<double2 *>(smem + gm.tab) + warp * (D / 2);
+    const int it = lane % SPR;  // a lane's slots are all slot `it` of a head
+    int c1, c2;
+    slot_vectors(it, a.rot, a.interleaved, c1, c2);
     for (int t = warp; t < nf; t += kWarps) {
         __syncwarp();
         for (int i = lane; i < half; i += 32) {
@@ -225,13 +232,14 @@ __global__ void __launch_bounds__(kThreads)
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) + tok * a.k_stride +
                                                            (size_t)h0 * D);
         uint4 *dst = keys + (fresh0 + t) * heads * CPR;
+        double2 cs[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cs[i] = tab[8 * it + i];
 #pragma unroll 2
         for (int e = lane; e < heads * SPR; e += 32) {
-            const int it = e % SPR, h = e / SPR;
-            int c1, c2;
-            slot_vectors(it, a.rot, a.interleaved, c1, c2);
+            const int h = e / SPR;
             uint4 x1 = src[h * CPR + c1], x2 = src[h * CPR + c2];
-            rotate_slot<double>(x1, x2, it, a.rot, a.interleaved, tab);
+            rotate_slot<double>(x1, x2, it, a.rot, a.interleaved, cs);
             dst[h * CPR + c1] = x1;
             dst[h * CPR + c2] = x2;
             if (!Q4) {
