@@ -78,23 +78,44 @@ __device__ __forceinline__ void fold2(uint32_t &mn, uint32_t &mx, uint32_t x) {
          (bf_hi(x) > bf_hi(mx) ? x & 0xffff0000u : mx & 0xffff0000u);
 }
 
-// A head row of D channels is D / 16 slots of two 16-byte vectors each: a pair of
-// vectors half a rotation apart, two vectors of adjacent pairs, or two that are
-// copied.  The vectors of slot it:
-__device__ __forceinline__ void slot_vectors(int it, int rot, int interleaved, int &c1, int &c2) {
-    const bool apart = it < rot / 16 && !interleaved;
-    c1 = apart ? it : 2 * it;
-    c2 = apart ? it + rot / 16 : 2 * it + 1;
+// A head row of D channels is D / 16 slots of two 16-byte vectors each, such that
+// neighbouring slots' vectors are neighbours: a pair of vectors half a rotation
+// apart, two vectors of adjacent pairs half a row apart, or two that are copied.
+struct Slot {
+    int c1, c2;    // the vectors
+    int f1, f2;    // first of the four frequencies of each half of the slot
+    bool r1, r2;   // rotated
+};
+template <int D>
+__device__ __forceinline__ Slot slot_of(int it, int rot, int interleaved) {
+    Slot s;
+    if (interleaved) {
+        s.c1 = it;
+        s.c2 = it + D / 16;
+        s.f1 = 4 * s.c1;
+        s.f2 = 4 * s.c2;
+    } else if (it < rot / 16) {
+        s.c1 = it;
+        s.c2 = it + rot / 16;
+        s.f1 = 8 * it;
+        s.f2 = 8 * it + 4;
+    } else {
+        s.c1 = rot / 16 + it;
+        s.c2 = it + D / 16;
+        s.f1 = s.f2 = 0;
+    }
+    s.r1 = s.c1 < rot / 8;
+    s.r2 = s.c2 < rot / 8;
+    return s;
 }
 // Rotate them; cs: (cos, sin) of the slot's eight frequencies.
 template <typename T, typename T2>
-__device__ __forceinline__ void rotate_slot(uint4 &x1, uint4 &x2, int it, int rot, int interleaved,
+__device__ __forceinline__ void rotate_slot(uint4 &x1, uint4 &x2, const Slot &s, int interleaved,
                                             const T2 (&cs)[8]) {
-    if (it >= rot / 16) return;
     if (interleaved) {
-        rotate4_adjacent<T>(x1, cs);
-        rotate4_adjacent<T>(x2, cs + 4);
-    } else {
+        if (s.r1) rotate4_adjacent<T>(x1, cs);
+        if (s.r2) rotate4_adjacent<T>(x2, cs + 4);
+    } else if (s.r1) {
         rotate8<T>(x1, x2, cs);
     }
 }
@@ -109,7 +130,7 @@ __device__ __forceinline__ void unpack16(const uint4 &x0, const uint4 &x1, float
 }
 
 template <int D, bool Q4>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     append_rope_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ AppendGeom gm,
                        uint32_t *err) {
     constexpr int CPR = D / 8;     // 16-byte vectors a row
@@ -134,10 +155,13 @@ __global__ void __launch_bounds__(kThreads)
     const int start = L - n;  // cache position of the first fresh token
     const int half = a.rot / 2;
 
-    if ((int)blockIdx.x >= gm.key_ctas) {  // ------------------------------- queries
+    // Key and query CTAs take turns along x, so that they share the SMs.
+    const int ctas = gridDim.x;
+    const int ki = (int)((long long)blockIdx.x * gm.key_ctas / ctas);
+    if ((int)(((long long)blockIdx.x + 1) * gm.key_ctas / ctas) == ki) {  // --------- queries
         // warps per token: 8 / q_tokens, each a share of the heads' slots
         const int wpt = kWarps / gm.q_tokens;
-        const int r = ((int)blockIdx.x - gm.key_ctas) * gm.q_tokens + warp / wpt;
+        const int r = ((int)blockIdx.x - ki) * gm.q_tokens + warp / wpt;
         if (r >= n) return;
         float2 *tab = reinterpret_cast<float2 *>(smem) + warp * (D / 2);
         for (int i = lane; i < half; i += 32) {
@@ -153,12 +177,10 @@ __global__ void __launch_bounds__(kThreads)
         const int slots = gm.hq * SPR, step = 32 * wpt;
         // a lane's slots are all slot `it` of a head: its angles stay in registers (read from
         // shared memory for each head they took most of the time)
-        const int it = lane % SPR;
-        int c1, c2;
-        slot_vectors(it, a.rot, a.interleaved, c1, c2);
+        const Slot sl = slot_of<D>(lane % SPR, a.rot, a.interleaved);
         float2 cs[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = tab[8 * it + i];
+        for (int i = 0; i < 8; ++i) cs[i] = tab[(i < 4 ? sl.f1 : sl.f2 - 4) + i];
         constexpr int kAhead = 4;
         for (int e0 = (warp % wpt) * 32 + lane; e0 < slots; e0 += kAhead * step) {
             uint4 x1[kAhead], x2[kAhead];
@@ -166,17 +188,17 @@ __global__ void __launch_bounds__(kThreads)
             for (int k = 0; k < kAhead; ++k) {
                 const int e = e0 + k * step;
                 if (e < slots) {
-                    x1[k] = src[e / SPR * CPR + c1];
-                    x2[k] = src[e / SPR * CPR + c2];
+                    x1[k] = src[e / SPR * CPR + sl.c1];
+                    x2[k] = src[e / SPR * CPR + sl.c2];
                 }
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int e = e0 + k * step;
                 if (e < slots) {
-                    rotate_slot<float>(x1[k], x2[k], it, a.rot, a.interleaved, cs);
-                    dst[e / SPR * CPR + c1] = x1[k];
-                    dst[e / SPR * CPR + c2] = x2[k];
+                    rotate_slot<float>(x1[k], x2[k], sl, a.interleaved, cs);
+                    dst[e / SPR * CPR + sl.c1] = x1[k];
+                    dst[e / SPR * CPR + sl.c2] = x2[k];
                 }
             }
         }
@@ -185,8 +207,8 @@ __global__ void __launch_bounds__(kThreads)
 
     // ------------------------------------------------------------ keys and values
     const int heads = 1 << gm.lg_heads, groups = gm.hkv >> gm.lg_heads;
-    const int blk = start / gm.bs + (int)blockIdx.x / groups;
-    const int h0 = ((int)blockIdx.x % groups) * heads;
+    const int blk = start / gm.bs + ki / groups;
+    const int h0 = (ki % groups) * heads;
     if (blk > (L - 1) / gm.bs) return;
     const int page = a.page_table[(size_t)row * gm.max_pages + blk];
     if (page < 0 || page >= gm.num_pages) {
@@ -215,12 +237,24 @@ __global__ void __launch_bounds__(kThreads)
             keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
         }
     }
-    // fresh keys, rotated, into shared memory (and the bf16 cache): a warp a token
+    // fresh keys, rotated, into shared memory (and the bf16 cache): a warp a token, whose
+    // vectors are on their way while its angles are worked out
     double2 *tab = reinterpret_cast<double2 *>(smem + gm.tab) + warp * (D / 2);
-    const int it = lane % SPR;  // a lane's slots are all slot `it` of a head
-    int c1, c2;
-    slot_vectors(it, a.rot, a.interleaved, c1, c2);
+    const Slot sl = slot_of<D>(lane % SPR, a.rot, a.interleaved);
+    constexpr int kAhead = D / 64;  // heads * SPR slots of at most 8 heads, 32 at a time
     for (int t = warp; t < nf; t += kWarps) {
+        const size_t tok = (size_t)b * a.f + r0 + t;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) + tok * a.k_stride +
+                                                           (size_t)h0 * D);
+        uint4 x1[kAhead], x2[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = (lane + 32 * k) / SPR;
+            if (h < heads) {
+                x1[k] = src[h * CPR + sl.c1];
+                x2[k] = src[h * CPR + sl.c2];
+            }
+        }
         __syncwarp();
         for (int i = lane; i < half; i += 32) {
             double s, c;
@@ -228,24 +262,22 @@ __global__ void __launch_bounds__(kThreads)
             tab[i] = make_double2(c * a.mscale, s * a.mscale);
         }
         __syncwarp();
-        const size_t tok = (size_t)b * a.f + r0 + t;
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) + tok * a.k_stride +
-                                                           (size_t)h0 * D);
         uint4 *dst = keys + (fresh0 + t) * heads * CPR;
         double2 cs[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = tab[8 * it + i];
-#pragma unroll 2
-        for (int e = lane; e < heads * SPR; e += 32) {
-            const int h = e / SPR;
-            uint4 x1 = src[h * CPR + c1], x2 = src[h * CPR + c2];
-            rotate_slot<double>(x1, x2, it, a.rot, a.interleaved, cs);
-            dst[h * CPR + c1] = x1;
-            dst[h * CPR + c2] = x2;
-            if (!Q4) {
-                uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + fresh0 + t) * CPR;
-                out[c1] = x1;
-                out[c2] = x2;
+        for (int i = 0; i < 8; ++i) cs[i] = tab[(i < 4 ? sl.f1 : sl.f2 - 4) + i];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = (lane + 32 * k) / SPR;
+            if (h < heads) {
+                rotate_slot<double>(x1[k], x2[k], sl, a.interleaved, cs);
+                dst[h * CPR + sl.c1] = x1[k];
+                dst[h * CPR + sl.c2] = x2[k];
+                if (!Q4) {
+                    uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + fresh0 + t) * CPR;
+                    out[sl.c1] = x1[k];
+                    out[sl.c2] = x2[k];
+                }
             }
         }
     }
