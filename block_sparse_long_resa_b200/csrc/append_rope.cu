@@ -3,13 +3,12 @@
 // expansion to bf16 pages (ReSA summary §3.2 "Block Key Cache", Eq. 3;
 // Algorithm 1 incremental updates, for any number of tokens).
 //
-// Grid (CTAs of keys and values, then CTAs of queries; batch).  A key CTA owns
-// one block of the cache that holds fresh tokens and a range of kv heads, so it
-// alone writes that block's slots and its descriptor: its warps take a token
-// each, bring the keys as stored (rotated, or read back from the cache below the
-// first fresh slot) into shared memory, and the CTA folds their min / max per
-// channel.  Of a query CTA a warp, or several where there are few tokens, takes a
-// token.  A warp works out its token's angles once, for all heads.
+// Grid (key CTAs and token CTAs in turns; batch).  A key CTA owns one block of the
+// cache that holds fresh tokens and a range of kv heads, so it alone writes that
+// block's keys and its descriptor: it brings the keys as stored (rotated, 16 tokens
+// at a time, or read back from the cache below the first fresh slot) into shared
+// memory and folds their min / max per channel.  Of a token CTA a warp, or several
+// where there are few tokens, takes a token: its queries and its values.
 //
 // An angle is pos * inv_freq in turns in fp64, reduced to [-1/2, 1/2] before
 // the sine, so that a position of 2^20 has as good an angle as position 1.  Keys
@@ -28,8 +27,8 @@ constexpr double kInvTwoPi = 0.15915494309189533577;
 struct AppendGeom {
     int hq, hkv, lg_heads;  // 2^lg_heads kv heads a key CTA takes
     int max_pages, num_pages, bs;
-    int key_ctas;        // CTAs of keys and values along x
-    int q_tokens;        // tokens a query CTA takes: 1, 2, 4 or 8
+    int key_ctas;        // CTAs of keys along x
+    int q_tokens;        // tokens a token CTA takes: 1, 2, 4 or 8
     int tab;             // byte offset of the angles in shared memory
     RowMap rm;
 };
@@ -120,15 +119,6 @@ __device__ __forceinline__ void rotate_slot(uint4 &x1, uint4 &x2, const Slot &s,
     }
 }
 
-__device__ __forceinline__ void unpack16(const uint4 &x0, const uint4 &x1, float (&x)[kQ4Group]) {
-    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[2 * i] = bf_lo(w[i]);
-        x[2 * i + 1] = bf_hi(w[i]);
-    }
-}
-
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kThreads, 3)
     append_rope_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ AppendGeom gm,
@@ -155,14 +145,40 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int start = L - n;  // cache position of the first fresh token
     const int half = a.rot / 2;
 
-    // Key and query CTAs take turns along x, so that they share the SMs.
+    // Key and token CTAs take turns along x, so that they share the SMs.
     const int ctas = gridDim.x;
     const int ki = (int)((long long)blockIdx.x * gm.key_ctas / ctas);
-    if ((int)(((long long)blockIdx.x + 1) * gm.key_ctas / ctas) == ki) {  // --------- queries
-        // warps per token: 8 / q_tokens, each a share of the heads' slots
-        const int wpt = kWarps / gm.q_tokens;
+    bool bad = false;
+    if ((int)(((long long)blockIdx.x + 1) * gm.key_ctas / ctas) == ki) {  // ---- a token's queries and values
+        // warps per token: 8 / q_tokens, each a share of the vectors
+        const int wpt = kWarps / gm.q_tokens, step = 32 * wpt;
         const int r = ((int)blockIdx.x - ki) * gm.q_tokens + warp / wpt;
         if (r >= n) return;
+        const size_t tok = (size_t)b * a.f + r;
+        const int pos = start + r;
+        const int page = a.page_table[(size_t)row * gm.max_pages + pos / gm.bs];
+        if (page >= 0 && page < gm.num_pages) {  // (the key CTA reports it)
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.vn) + tok * a.v_stride);
+            const size_t slot0 = (size_t)page * gm.hkv * gm.bs + pos % gm.bs;
+#pragma unroll 2
+            for (int e = (warp % wpt) * 32 + lane; e < gm.hkv * (Q4 ? SPR : CPR); e += step) {
+                if (Q4) {
+                    const int h = e / SPR;
+                    const uint4 x0 = src[2 * e], x1 = src[2 * e + 1];
+                    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                    uint2 codes;
+                    uint32_t sf;
+                    bad |= q4_quantise(w, 1.f / head_scale(a.v_scale, h), codes, sf);
+                    const size_t at = (slot0 + (size_t)h * gm.bs) * SPR + e % SPR;
+                    static_cast<uint2 *>(a.v)[at] = codes;
+                    static_cast<uint8_t *>(a.v_sf)[at] = (uint8_t)sf;
+                } else {
+                    static_cast<uint4 *>(a.v)[(slot0 + (size_t)(e / CPR) * gm.bs) * CPR + e % CPR] = src[e];
+                }
+            }
+        }
+        if (Q4 && bad) set_error(err, RESA_DEVERR_NONFINITE);
+        if (!a.q) return;
         float2 *tab = reinterpret_cast<float2 *>(smem) + warp * (D / 2);
         for (int i = lane; i < half; i += 32) {
             float s, c;
@@ -171,10 +187,9 @@ __global__ void __launch_bounds__(kThreads, 3)
             tab[i] = make_float2(c * m, s * m);
         }
         __syncwarp();
-        const size_t tok = (size_t)b * a.f + r;
         const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + tok * a.q_stride);
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.q_out) + tok * gm.hq * D);
-        const int slots = gm.hq * SPR, step = 32 * wpt;
+        const int slots = gm.hq * SPR;
         // a lane's slots are all slot `it` of a head: its angles stay in registers (read from
         // shared memory for each head they took most of the time)
         const Slot sl = slot_of<D>(lane % SPR, a.rot, a.interleaved);
@@ -205,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         return;
     }
 
-    // ------------------------------------------------------------ keys and values
+    // ----------------------------------------------------------------------- keys
     const int heads = 1 << gm.lg_heads, groups = gm.hkv >> gm.lg_heads;
     const int blk = start / gm.bs + ki / groups;
     const int h0 = (ki % groups) * heads;
@@ -220,9 +235,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int valid = min(gm.bs, L - pos0);                    // slots of the block below seq_len
     const int fresh0 = max(0, start - pos0);                   // the first fresh one
     const int r0 = pos0 + fresh0 - start;                      // its row in the call's arrays
-    const int nf = valid - fresh0;
     const size_t prow = (size_t)page * gm.hkv + h0;            // (page, head) row base
-    bool bad = false;
 
     // keys below the first fresh slot, as stored
     for (int e = tid; e < fresh0 * heads * CPR; e += kThreads) {
@@ -237,93 +250,83 @@ __global__ void __launch_bounds__(kThreads, 3)
             keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
         }
     }
-    // fresh keys, rotated, into shared memory (and the bf16 cache): a warp a token, whose
-    // vectors are on their way while its angles are worked out
-    double2 *tab = reinterpret_cast<double2 *>(smem + gm.tab) + warp * (D / 2);
-    const Slot sl = slot_of<D>(lane % SPR, a.rot, a.interleaved);
-    constexpr int kAhead = D / 64;  // heads * SPR slots of at most 8 heads, 32 at a time
-    for (int t = warp; t < nf; t += kWarps) {
-        const size_t tok = (size_t)b * a.f + r0 + t;
-        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) + tok * a.k_stride +
-                                                           (size_t)h0 * D);
+    // fresh keys, rotated, into shared memory (and the bf16 cache), 16 tokens at a time;
+    // a thread's first vectors are on their way while the angles are worked out.  Angle
+    // i lies at i ^ (i / 8 % 8), so that eight lanes with eight slots meet all banks.
+    double2 *tab = reinterpret_cast<double2 *>(smem + gm.tab);  // [16][D / 2]
+    const Slot sl = slot_of<D>(tid % SPR, a.rot, a.interleaved);
+    const int lg_row = gm.lg_heads + (D == 128 ? 3 : 2);  // slots of a token: 2^lg_row
+    for (int t0 = fresh0; t0 < valid; t0 += kTileRows) {
+        const int nt = min(kTileRows, valid - t0), slots = nt << lg_row;
+        const size_t tok0 = (size_t)b * a.f + r0 + t0 - fresh0;
+        auto src_of = [&](int e) -> const uint4 * {
+            return reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) +
+                                                   (tok0 + (e >> lg_row)) * a.k_stride +
+                                                   (size_t)(h0 + (e / SPR & (heads - 1))) * D);
+        };
+        constexpr int kAhead = 2;
         uint4 x1[kAhead], x2[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int h = (lane + 32 * k) / SPR;
-            if (h < heads) {
-                x1[k] = src[h * CPR + sl.c1];
-                x2[k] = src[h * CPR + sl.c2];
+        for (int k = 0; k < kAhead; ++k)
+            if (tid + k * kThreads < slots) {
+                const uint4 *src = src_of(tid + k * kThreads);
+                x1[k] = src[sl.c1];
+                x2[k] = src[sl.c2];
             }
-        }
-        __syncwarp();
-        for (int i = lane; i < half; i += 32) {
+        if (t0 > fresh0) __syncthreads();
+#pragma unroll 2
+        for (int e = tid; e < nt * half; e += kThreads) {
+            const int t = e / half, i = e - t * half;
             double s, c;
-            sincospi(2.0 * turns(a, b, r0 + t, start + r0 + t, i), &s, &c);
-            tab[i] = make_double2(c * a.mscale, s * a.mscale);
+            sincospi(2.0 * turns(a, b, r0 + t0 - fresh0 + t, pos0 + t0 + t, i), &s, &c);
+            tab[t * (D / 2) + (i ^ (i / 8 % 8))] = make_double2(c * a.mscale, s * a.mscale);
         }
-        __syncwarp();
-        uint4 *dst = keys + (fresh0 + t) * heads * CPR;
-        double2 cs[8];
+        __syncthreads();
+        for (int e0 = tid; e0 < slots; e0 += kAhead * kThreads) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cs[i] = tab[(i < 4 ? sl.f1 : sl.f2 - 4) + i];
+            for (int k = 0; k < kAhead; ++k) {
+                const int e = e0 + k * kThreads;
+                if (e >= slots) break;
+                if (e0 != tid) {
+                    const uint4 *src = src_of(e);
+                    x1[k] = src[sl.c1];
+                    x2[k] = src[sl.c2];
+                }
+                const int t = e >> lg_row, h = e / SPR & (heads - 1);
+                double2 cs[8];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int h = (lane + 32 * k) / SPR;
-            if (h < heads) {
+                for (int i = 0; i < 8; ++i) {
+                    const int f = (i < 4 ? sl.f1 : sl.f2 - 4) + i;
+                    cs[i] = tab[t * (D / 2) + (f ^ (f / 8 % 8))];
+                }
                 rotate_slot<double>(x1[k], x2[k], sl, a.interleaved, cs);
-                dst[h * CPR + sl.c1] = x1[k];
-                dst[h * CPR + sl.c2] = x2[k];
+                uint4 *dst = keys + ((t0 + t) * heads + h) * CPR;
+                dst[sl.c1] = x1[k];
+                dst[sl.c2] = x2[k];
                 if (!Q4) {
-                    uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + fresh0 + t) * CPR;
+                    uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + t0 + t) * CPR;
                     out[sl.c1] = x1[k];
                     out[sl.c2] = x2[k];
                 }
             }
         }
     }
-    // values
-    if (Q4) {
-        for (int e = tid; e < nf * heads * SPR; e += kThreads) {
-            const int gi = e % SPR, th = e / SPR;
-            const int h = th & (heads - 1), t = th >> gm.lg_heads;
-            const size_t tok = (size_t)b * a.f + r0 + t;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const uint16_t *>(a.vn) + tok * a.v_stride + (size_t)(h0 + h) * D + gi * 16);
-            float x[kQ4Group];
-            unpack16(src[0], src[1], x);
-            uint2 codes;
-            uint32_t sf;
-            bad |= q4_quantise(x, 1.f / head_scale(a.v_scale, h0 + h), codes, sf);
-            const size_t slot = (prow + h) * gm.bs + fresh0 + t;
-            static_cast<uint2 *>(a.v)[slot * SPR + gi] = codes;
-            static_cast<uint8_t *>(a.v_sf)[slot * SPR + gi] = (uint8_t)sf;
-        }
-    } else {
-#pragma unroll 4
-        for (int e = tid; e < nf * heads * CPR; e += kThreads) {
-            const int c = e % CPR, th = e / CPR;
-            const int h = th & (heads - 1), t = th >> gm.lg_heads;
-            const size_t tok = (size_t)b * a.f + r0 + t;
-            static_cast<uint4 *>(a.v)[((prow + h) * gm.bs + fresh0 + t) * CPR + c] = reinterpret_cast<const uint4 *>(
-                static_cast<const uint16_t *>(a.vn) + tok * a.v_stride + (size_t)(h0 + h) * D)[c];
-        }
-    }
     __syncthreads();
     if (Q4) {
         // 4-bit codes of the fresh keys; shared memory then holds what they stand for
-        for (int e = tid; e < nf * heads * SPR; e += kThreads) {
+        for (int e = tid; e < (valid - fresh0) * heads * SPR; e += kThreads) {
             const int gi = e % SPR, th = e / SPR;
-            const int h = th & (heads - 1), t = th >> gm.lg_heads;
-            uint4 *kp = keys + ((fresh0 + t) * heads + h) * CPR + 2 * gi;
-            float x[kQ4Group];
-            unpack16(kp[0], kp[1], x);
+            const int h = th & (heads - 1), t = fresh0 + (th >> gm.lg_heads);
+            uint4 *kp = keys + (t * heads + h) * CPR + 2 * gi;
+            const uint4 x0 = kp[0], x1 = kp[1];
+            const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
             const float g = head_scale(a.k_scale, h0 + h);
             uint2 codes;
             uint32_t sf;
-            bad |= q4_quantise(x, 1.f / g, codes, sf);
-            const size_t slot = (prow + h) * gm.bs + fresh0 + t;
-            static_cast<uint2 *>(a.k)[slot * SPR + gi] = codes;
-            static_cast<uint8_t *>(a.k_sf)[slot * SPR + gi] = (uint8_t)sf;
+            bad |= q4_quantise(w, 1.f / g, codes, sf);
+            const size_t at = ((prow + h) * gm.bs + t) * SPR + gi;
+            static_cast<uint2 *>(a.k)[at] = codes;
+            static_cast<uint8_t *>(a.k_sf)[at] = (uint8_t)sf;
             kp[0] = q4_values_bf16(codes.x, sf, g);
             kp[1] = q4_values_bf16(codes.y, sf, g);
         }
@@ -444,13 +447,13 @@ cudaError_t launch_append_t(const Shape &s, const AppendArgs &a, uint32_t *err, 
     const int blocks = (int)(((long long)a.f + s.bs - 2) / s.bs + 1);  // blocks f tokens can touch
     gm.key_ctas = (blocks < s.max_pages ? blocks : s.max_pages) * (s.hkv / heads);
     gm.q_tokens = a.f >= kWarps ? kWarps : a.f >= 4 ? 4 : a.f >= 2 ? 2 : 1;
-    const int query_ctas = a.q ? (a.f - 1) / gm.q_tokens + 1 : 0;
-    constexpr int most = kKeyRows * D * 2 + kWarps * (D / 2) * 16;
+    const int token_ctas = (a.f - 1) / gm.q_tokens + 1;
+    constexpr int tab = kTileRows * (D / 2) * 16, most = kKeyRows * D * 2 + tab;
     static std::atomic<int> done[64];
     cudaError_t e = ensure_smem(append_rope_kernel<D, Q4>, most, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(append_rope_kernel<D, Q4>, dim3(gm.key_ctas + query_ctas, s.batch),
-                      dim3(kThreads), gm.tab + kWarps * (D / 2) * 16, st, a, gm, err);
+    return launch_pdl(append_rope_kernel<D, Q4>, dim3(gm.key_ctas + token_ctas, s.batch),
+                      dim3(kThreads), gm.tab + tab, st, a, gm, err);
 }
 
 }  // namespace

@@ -60,38 +60,57 @@ __device__ __forceinline__ float f16_hi(uint32_t p) {
     return __half2float(__ushort_as_half((unsigned short)(p >> 16)));
 }
 
-// Quantise one group x[0..15] with 1/g = rg: codes (channel i in nibble i) and
-// the e4m3 scale byte.  The code of y is the number of e2m1 decision points
-// t * s it passes; t * s is exact in fp32 (3 + 4 bits), so no quotient y / s is
-// rounded and ties go to the even code, as e2m1's nearest-even does.  NaN
-// counts as 0 and infinity saturates; returns whether either occurred.
-__device__ __forceinline__ bool q4_quantise(const float (&x)[kQ4Group], float rg, uint2 &codes,
+// Quantise one group of 16 bf16 values (pairs, channel 0 low) with 1/g = rg: codes
+// (channel i in nibble i) and the e4m3 scale byte.  A code is the nearest e2m1 of
+// y / s with the quotient correctly rounded (a reciprocal, and one residual step
+// after Markstein, 1990): ties, y = t * s for a decision point t of at most 3 bits,
+// then stay ties, and no y beside one is rounded onto it, since y and the quotient
+// have 24 bits both.  (Counting the seven decision points that |y| passes took five
+// times the instructions.)  NaN counts as 0 and infinity saturates; returns
+// whether either occurred.
+__device__ __forceinline__ bool q4_quantise(const uint32_t (&w)[8], float rg, uint2 &codes,
                                             uint32_t &sf) {
-    float y[kQ4Group], amax = 0.f;
-    bool finite = true;
+    uint32_t m2 = 0;
 #pragma unroll
-    for (int i = 0; i < kQ4Group; ++i) {
-        y[i] = x[i] * rg;
-        amax = fmaxf(amax, fabsf(y[i]));
-        finite = finite && (fabsf(y[i]) < INFINITY);
+    for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7fff7fffu);
+    const uint32_t mag = max(m2 & 0xffffu, m2 >> 16);
+    float amax = bf16_bits_to_f32((uint16_t)mag) * rg;  // rounding keeps the order
+    float y[kQ4Group];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        y[2 * i] = bf_lo(w[i]) * rg;
+        y[2 * i + 1] = bf_hi(w[i]) * rg;
+    }
+    const bool finite = amax < INFINITY;
+    if (!finite) {
+        amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < kQ4Group; ++i) {
+            y[i] = y[i] == y[i] ? fminf(fmaxf(y[i], -3e38f), 3e38f) : 0.f;
+            amax = fmaxf(amax, fabsf(y[i]));
+        }
     }
     sf = f32_to_e4m3(__fdiv_rn(amax, 6.f));
     const float s = e4m3_to_f32(sf);
-    codes = make_uint2(0u, 0u);
-    if (s > 0.f) {
-        const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s,
-                    t5 = 3.5f * s, t6 = 5.f * s;
+    const float rs = s > 0.f ? __frcp_rn(s) : 0.f;
 #pragma unroll
-        for (int i = 0; i < kQ4Group; ++i) {
-            const float a = fabsf(y[i]);
-            uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
-            c |= y[i] < 0.f ? 8u : 0u;
-            if (i < 8)
-                codes.x |= c << (4 * i);
-            else
-                codes.y |= c << (4 * (i - 8));
-        }
+    for (int i = 0; i < kQ4Group; ++i) {
+        const float q = y[i] * rs;
+        y[i] = fmaf(fmaf(-q, s, y[i]), rs, q);
     }
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+            "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+            : "=r"(c[i])
+            : "f"(y[8 * i]), "f"(y[8 * i + 1]), "f"(y[8 * i + 2]), "f"(y[8 * i + 3]), "f"(y[8 * i + 4]),
+              "f"(y[8 * i + 5]), "f"(y[8 * i + 6]), "f"(y[8 * i + 7]));
+    codes = s > 0.f ? make_uint2(c[0], c[1]) : make_uint2(0u, 0u);
     return !finite;
 }
 
