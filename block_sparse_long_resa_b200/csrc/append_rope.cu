@@ -5,8 +5,8 @@
 //
 // Grid (key CTAs and token CTAs in turns; batch).  A key CTA owns one block of the
 // cache that holds fresh tokens and a range of kv heads, so it alone writes that
-// block's keys and its descriptor: it brings the keys as stored (rotated, 16 tokens
-// at a time, or read back from the cache below the first fresh slot) into shared
+// block's keys and its descriptor: 16 tokens at a time it brings the keys as stored
+// (rotated, or read back from the cache below the first fresh slot) into shared
 // memory and folds their min / max per channel.  Of a token CTA a warp, or several
 // where there are few tokens, takes a token: its queries and its values.
 //
@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKeyRows = 256;  // most (token, head) rows of keys a CTA holds, D channels each
 constexpr double kInvTwoPi = 0.15915494309189533577;
 
 struct AppendGeom {
@@ -29,7 +28,6 @@ struct AppendGeom {
     int max_pages, num_pages, bs;
     int key_ctas;        // CTAs of keys along x
     int q_tokens;        // tokens a token CTA takes: 1, 2, 4 or 8
-    int tab;             // byte offset of the angles in shared memory
     RowMap rm;
 };
 
@@ -230,40 +228,34 @@ __global__ void __launch_bounds__(kThreads, 3)
         if (tid == 0) set_error(err, RESA_DEVERR_PAGE);
         return;
     }
-    uint4 *keys = reinterpret_cast<uint4 *>(smem);  // [token][head][CPR]
+    uint4 *keys = reinterpret_cast<uint4 *>(smem);  // [16][head][CPR]
+    // Angle i of a token lies at i ^ (i / 8 % 8), so that eight lanes with eight slots
+    // meet all banks.
+    double2 *tab = reinterpret_cast<double2 *>(smem + (kTileRows * D * 2 << gm.lg_heads));  // [16][D / 2]
     const int pos0 = blk * gm.bs;
-    const int valid = min(gm.bs, L - pos0);                    // slots of the block below seq_len
-    const int fresh0 = max(0, start - pos0);                   // the first fresh one
-    const int r0 = pos0 + fresh0 - start;                      // its row in the call's arrays
-    const size_t prow = (size_t)page * gm.hkv + h0;            // (page, head) row base
-
-    // keys below the first fresh slot, as stored
-    for (int e = tid; e < fresh0 * heads * CPR; e += kThreads) {
-        const int c = e % CPR, th = e / CPR;
-        const int h = th & (heads - 1), t = th >> gm.lg_heads;
-        const size_t slot = (prow + h) * gm.bs + t;
-        if (Q4) {
-            const uint32_t w = static_cast<const uint32_t *>(a.k)[slot * CPR + c];
-            const uint32_t sf = static_cast<const uint8_t *>(a.k_sf)[slot * SPR + c / 2];
-            keys[e] = q4_values_bf16(w, sf, head_scale(a.k_scale, h0 + h));
-        } else {
-            keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
-        }
-    }
-    // fresh keys, rotated, into shared memory (and the bf16 cache), 16 tokens at a time;
-    // a thread's first vectors are on their way while the angles are worked out.  Angle
-    // i lies at i ^ (i / 8 % 8), so that eight lanes with eight slots meet all banks.
-    double2 *tab = reinterpret_cast<double2 *>(smem + gm.tab);  // [16][D / 2]
-    const Slot sl = slot_of<D>(tid % SPR, a.rot, a.interleaved);
+    const int valid = min(gm.bs, L - pos0);          // slots of the block below seq_len
+    const int fresh0 = max(0, start - pos0);         // the first fresh one
+    const size_t prow = (size_t)page * gm.hkv + h0;  // (page, head) row base
     const int lg_row = gm.lg_heads + (D == 128 ? 3 : 2);  // slots of a token: 2^lg_row
-    for (int t0 = fresh0; t0 < valid; t0 += kTileRows) {
-        const int nt = min(kTileRows, valid - t0), slots = nt << lg_row;
-        const size_t tok0 = (size_t)b * a.f + r0 + t0 - fresh0;
+    const Slot sl = slot_of<D>(tid % SPR, a.rot, a.interleaved);
+    constexpr int kFold = kMaxKvHeads * (D / 2) / kThreads;  // channel pairs a thread folds
+    uint32_t mn[kFold], mx[kFold];
+#pragma unroll
+    for (int j = 0; j < kFold; ++j) mn[j] = mx[j] = 0u;
+
+#pragma unroll 1
+    for (int t0 = 0; t0 < valid; t0 += kTileRows) {
+        const int nt = min(kTileRows, valid - t0);
+        const int old = max(0, min(nt, fresh0 - t0));                   // keys that are there already
+        const int nf = nt - old;
+        const int r0 = pos0 + t0 + old - start;                         // the first fresh one's row
+        const int slots = nf << lg_row;
         auto src_of = [&](int e) -> const uint4 * {
             return reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) +
-                                                   (tok0 + (e >> lg_row)) * a.k_stride +
+                                                   ((size_t)b * a.f + r0 + (e >> lg_row)) * a.k_stride +
                                                    (size_t)(h0 + (e / SPR & (heads - 1))) * D);
         };
+        // a thread's first vectors are on their way while the angles are worked out
         constexpr int kAhead = 2;
         uint4 x1[kAhead], x2[kAhead];
 #pragma unroll
@@ -273,13 +265,25 @@ __global__ void __launch_bounds__(kThreads, 3)
                 x1[k] = src[sl.c1];
                 x2[k] = src[sl.c2];
             }
-        if (t0 > fresh0) __syncthreads();
+        if (t0) __syncthreads();
 #pragma unroll 2
-        for (int e = tid; e < nt * half; e += kThreads) {
+        for (int e = tid; e < nf * half; e += kThreads) {
             const int t = e / half, i = e - t * half;
             double s, c;
-            sincospi(2.0 * turns(a, b, r0 + t0 - fresh0 + t, pos0 + t0 + t, i), &s, &c);
+            sincospi(2.0 * turns(a, b, r0 + t, start + r0 + t, i), &s, &c);
             tab[t * (D / 2) + (i ^ (i / 8 % 8))] = make_double2(c * a.mscale, s * a.mscale);
+        }
+        for (int e = tid; e < old * heads * CPR; e += kThreads) {
+            const int c = e % CPR, th = e / CPR;
+            const int h = th & (heads - 1), t = t0 + (th >> gm.lg_heads);
+            const size_t slot = (prow + h) * gm.bs + t;
+            if (Q4) {
+                const uint32_t w = static_cast<const uint32_t *>(a.k)[slot * CPR + c];
+                const uint32_t sf = static_cast<const uint8_t *>(a.k_sf)[slot * SPR + c / 2];
+                keys[e] = q4_values_bf16(w, sf, head_scale(a.k_scale, h0 + h));
+            } else {
+                keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
+            }
         }
         __syncthreads();
         for (int e0 = tid; e0 < slots; e0 += kAhead * kThreads) {
@@ -300,48 +304,56 @@ __global__ void __launch_bounds__(kThreads, 3)
                     cs[i] = tab[t * (D / 2) + (f ^ (f / 8 % 8))];
                 }
                 rotate_slot<double>(x1[k], x2[k], sl, a.interleaved, cs);
-                uint4 *dst = keys + ((t0 + t) * heads + h) * CPR;
+                uint4 *dst = keys + ((old + t) * heads + h) * CPR;
                 dst[sl.c1] = x1[k];
                 dst[sl.c2] = x2[k];
                 if (!Q4) {
-                    uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + t0 + t) * CPR;
+                    uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + t0 + old + t) * CPR;
                     out[sl.c1] = x1[k];
                     out[sl.c2] = x2[k];
                 }
             }
         }
-    }
-    __syncthreads();
-    if (Q4) {
-        // 4-bit codes of the fresh keys; shared memory then holds what they stand for
-        for (int e = tid; e < (valid - fresh0) * heads * SPR; e += kThreads) {
-            const int gi = e % SPR, th = e / SPR;
-            const int h = th & (heads - 1), t = fresh0 + (th >> gm.lg_heads);
-            uint4 *kp = keys + (t * heads + h) * CPR + 2 * gi;
-            const uint4 x0 = kp[0], x1 = kp[1];
-            const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-            const float g = head_scale(a.k_scale, h0 + h);
-            uint2 codes;
-            uint32_t sf;
-            bad |= q4_quantise(w, 1.f / g, codes, sf);
-            const size_t at = ((prow + h) * gm.bs + t) * SPR + gi;
-            static_cast<uint2 *>(a.k)[at] = codes;
-            static_cast<uint8_t *>(a.k_sf)[at] = (uint8_t)sf;
-            kp[0] = q4_values_bf16(codes.x, sf, g);
-            kp[1] = q4_values_bf16(codes.y, sf, g);
-        }
         __syncthreads();
-    }
-    // descriptors: a thread two channels of a head
-    const uint32_t *kw = reinterpret_cast<const uint32_t *>(keys);
-    const int width = heads * (D / 2);
-    for (int e = tid; e < width; e += kThreads) {
-        uint32_t mn = kw[e], mx = mn;
+        if (Q4) {
+            // 4-bit codes of the fresh keys; shared memory then holds what they stand for
+            for (int e = tid; e < slots; e += kThreads) {
+                const int gi = e % SPR, h = e / SPR & (heads - 1), t = old + (e >> lg_row);
+                uint4 *kp = keys + (t * heads + h) * CPR + 2 * gi;
+                const uint4 y0 = kp[0], y1 = kp[1];
+                const uint32_t w[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+                const float g = head_scale(a.k_scale, h0 + h);
+                uint2 codes;
+                uint32_t sf;
+                bad |= q4_quantise(w, 1.f / g, codes, sf);
+                const size_t at = ((prow + h) * gm.bs + t0 + t) * SPR + gi;
+                static_cast<uint2 *>(a.k)[at] = codes;
+                static_cast<uint8_t *>(a.k_sf)[at] = (uint8_t)sf;
+                kp[0] = q4_values_bf16(codes.x, sf, g);
+                kp[1] = q4_values_bf16(codes.y, sf, g);
+            }
+            __syncthreads();
+        }
+        // descriptors: a thread two channels of a head
+        const uint32_t *kw = reinterpret_cast<const uint32_t *>(keys);
+#pragma unroll
+        for (int j = 0; j < kFold; ++j) {
+            const int e = tid + j * kThreads, width = heads * (D / 2);
+            if (e < width) {
+                if (t0 == 0) mn[j] = mx[j] = kw[e];
 #pragma unroll 4
-        for (int t = 1; t < valid; ++t) fold2(mn, mx, kw[t * width + e]);
-        uint32_t *d = static_cast<uint32_t *>(a.desc) + (prow + e / (D / 2)) * D + e % (D / 2);  // [2][D / 2] words
-        d[0] = mn;
-        d[D / 2] = mx;
+                for (int t = t0 == 0; t < nt; ++t) fold2(mn[j], mx[j], kw[t * width + e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kFold; ++j) {
+        const int e = tid + j * kThreads;
+        if (e < heads * (D / 2)) {
+            uint32_t *d = static_cast<uint32_t *>(a.desc) + (prow + e / (D / 2)) * D + e % (D / 2);  // [2][D / 2] words
+            d[0] = mn[j];
+            d[D / 2] = mx[j];
+        }
     }
     if (Q4 && bad) set_error(err, RESA_DEVERR_NONFINITE);
 }
@@ -437,23 +449,22 @@ cudaError_t launch_append_t(const Shape &s, const AppendArgs &a, uint32_t *err, 
     AppendGeom gm{};
     gm.hq = s.hq;
     gm.hkv = s.hkv;
-    const int heads = s.hkv < kKeyRows / s.bs ? s.hkv : kKeyRows / s.bs;
-    gm.lg_heads = heads == 8 ? 3 : heads == 4 ? 2 : heads == 2 ? 1 : 0;
-    gm.tab = s.bs * heads * D * 2;
     gm.max_pages = s.max_pages;
     gm.num_pages = s.num_pages;
     gm.bs = s.bs;
     gm.rm = s.rows;
-    const int blocks = (int)(((long long)a.f + s.bs - 2) / s.bs + 1);  // blocks f tokens can touch
-    gm.key_ctas = (blocks < s.max_pages ? blocks : s.max_pages) * (s.hkv / heads);
+    long long blocks = ((long long)a.f + s.bs - 2) / s.bs + 1;  // blocks f tokens can touch
+    if (blocks > s.max_pages) blocks = s.max_pages;
+    // All heads a CTA, so that the angles are worked out once, unless that leaves too few CTAs.
+    int lg_heads = s.hkv == 8 ? 3 : s.hkv == 4 ? 2 : s.hkv == 2 ? 1 : 0;
+    while (lg_heads > 0 && blocks * s.batch * (s.hkv >> lg_heads) < 2 * kNumSms) --lg_heads;
+    gm.lg_heads = lg_heads;
+    gm.key_ctas = (int)blocks * (s.hkv >> lg_heads);
     gm.q_tokens = a.f >= kWarps ? kWarps : a.f >= 4 ? 4 : a.f >= 2 ? 2 : 1;
     const int token_ctas = (a.f - 1) / gm.q_tokens + 1;
-    constexpr int tab = kTileRows * (D / 2) * 16, most = kKeyRows * D * 2 + tab;
-    static std::atomic<int> done[64];
-    cudaError_t e = ensure_smem(append_rope_kernel<D, Q4>, most, done);
-    if (e != cudaSuccess) return e;
+    const int smem = (kTileRows * D * 2 << lg_heads) + kTileRows * (D / 2) * 16;  // at most 48 KB
     return launch_pdl(append_rope_kernel<D, Q4>, dim3(gm.key_ctas + token_ctas, s.batch),
-                      dim3(kThreads), gm.tab + tab, st, a, gm, err);
+                      dim3(kThreads), smem, st, a, gm, err);
 }
 
 }  // namespace
