@@ -35,6 +35,11 @@ template <int D, int NT>
 struct Q4Warps {
     static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 4 : 4;
 };
+// Units of at most so many keys are not split, by the width of the query tile.  Measured
+// (28 q / 4 kv heads, d 128, batch 1, 8, 32): 1024 keys 11 us whole and 16, 16, 19 us split,
+// 2048 keys 16-17 and 16, 17, 24, 4096 keys 26-27 and 12, 20, 33; with 16 heads a group 512
+// keys 11 and 12-13 us, 1024 keys 15 and 13, 13, 24.
+constexpr int kWholeKeys[2] = {2048, 768};
 constexpr float kShift = 13.f;     // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 2.f;      // growth of the maximum tolerated before rescaling
 
@@ -140,7 +145,6 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     constexpr int kWarps = SM::kWarps, kStages = SM::kStages, kThreads = 32 * kWarps;
     constexpr int kWords = D / 32;   // 32-bit words of codes a lane takes per K row
     constexpr int kRows = NT * 8;
-    constexpr int kItems = (kRows * (D / 4) + kThreads - 1) / kThreads;  // 4 channels each
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int sh_sum[kWarps], sh_unit, sh_first;
     __shared__ int4 sh_units[kThreads];  // (blocks, length, fresh tokens, row) when they fit
@@ -190,50 +194,59 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     };
 
     if (tid < 2) sh_part[tid].rows = 0;
-    // Prefix sums of the units' blocks: thread t sums units [t * per, ...).
+    // Whole units (no grid barrier): CTA u takes unit u.  Else prefix sums of the units'
+    // blocks: thread t sums units [t * per, ...).
+    const bool split = a.grid_bar != nullptr;
     const int per = (units + kThreads - 1) / kThreads;
-    const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
-    int mine = 0;
-    for (int u = u_lo; u < u_hi; ++u) {
-        const Unit x = unit_of(u, false);
-        mine += x.cnt;
-        if (per == 1) sh_units[u] = make_int4(x.cnt, x.L, x.n, x.row);
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sh_sum[warp] = incl;
-    __syncthreads();
-    int before = 0, W = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh_sum[w];
-        W += sh_sum[w];
-    }
-    incl += before;
-    // CTAs that take work: enough for a step of every warp each
-    const int least = max(1, 32 * kWarps / a.bs);
-    int G = max(1, min((int)gridDim.x, (W + least - 1) / least));
-    // With many CTAs a unit, as many for each: equal units then begin with a CTA's share.
-    if (G >= 8 * units) G -= G % units;
+    const bool kept = per == 1 && split;  // the units' data are in sh_units
+    int W = 0, G = 1, x0 = 0, x1 = 0;
     auto entry_of = [&](int q) -> int { return q < G ? (int)((long long)W * q / G) : W; };
-    const int x0 = entry_of(cta), x1 = entry_of(cta + 1);
-    if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
-        int s = incl - mine;
+    if (split) {
+        const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
+        int mine = 0;
         for (int u = u_lo; u < u_hi; ++u) {
-            const int k = per == 1 ? mine : unit_of(u, false).cnt;
-            if (x0 < s + k) {
-                sh_unit = u;
-                sh_first = s;
-                break;
-            }
-            s += k;
+            const Unit x = unit_of(u, false);
+            mine += x.cnt;
+            if (kept) sh_units[u] = make_int4(x.cnt, x.L, x.n, x.row);
         }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh_sum[warp] = incl;
+        __syncthreads();
+        int before = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sh_sum[w];
+            W += sh_sum[w];
+        }
+        incl += before;
+        // CTAs that take work: enough for a step of every warp each, or one a unit
+        const int least = max(1, 32 * kWarps / a.bs);
+        G = max(1, min(min((int)gridDim.x, W), max(units, (W + least - 1) / least)));
+        // With many CTAs a unit, as many for each: equal units then begin with a CTA's share.
+        if (G >= 8 * units) G -= G % units;
+        x0 = entry_of(cta);
+        x1 = entry_of(cta + 1);
+        if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
+            int s = incl - mine;
+            for (int u = u_lo; u < u_hi; ++u) {
+                const int k = kept ? mine : unit_of(u, false).cnt;
+                if (x0 < s + k) {
+                    sh_unit = u;
+                    sh_first = s;
+                    break;
+                }
+                s += k;
+            }
+        }
+        __syncthreads();
+    } else {
+        x1 = unit_of(cta, false).cnt;
     }
-    __syncthreads();
 
     auto orow_of = [&](int b, int h, int rho) -> size_t {
         return ((size_t)b * a.f + rho / a.g) * a.hq + (size_t)h * a.g + rho % a.g;
@@ -247,15 +260,15 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     auto lse_of = [&](float ms, float ls) -> float {
         return ls > 0.f ? (ms - kShift + log2f(ls)) * 0.6931471805599453f : ls == 0.f ? -INFINITY : ls;
     };
-    int u = x0 < x1 ? sh_unit : 0;
-    int ustart = x0 < x1 ? sh_first : 0;
+    int u = !split ? cta : x0 < x1 ? sh_unit : 0;
+    int ustart = split && x0 < x1 ? sh_first : 0;
     const int sub_shift = a.bs == 64 ? 2 : a.bs == 32 ? 1 : 0;  // tiles a block
     uint8_t *ring = smem + (size_t)warp * kStages * SM::kStage;
     const uint32_t ring_s = smem_u32(ring);
 
     for (int x = x0; x < x1; ++u) {
         Unit un;
-        if (per == 1) {
+        if (kept) {
             const int4 x4 = sh_units[u];
             un.b = u / a.hkv;
             un.h = u - un.b * a.hkv;
@@ -684,7 +697,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
 
     // Merge the units that span CTAs: behind a grid barrier each of a unit's CTAs takes
     // an equal share of its (row, four channels) items, with gl lanes an item, a lane a part.
-    if (gridDim.x > 1) {
+    if (split && gridDim.x > 1) {
         __threadfence();
         __syncthreads();
         if (tid == 0) sh_ok = grid_barrier_bounded(a.grid_bar, gridDim.x) ? 1u : 0u;
@@ -750,7 +763,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
 
     // Units without any block: zeros and -inf, and the errors of every unit.
     for (int u = cta; u < units; u += gridDim.x) {
-        if (per == 1 && sh_units[u].x > 0) continue;
+        if (kept && sh_units[u].x > 0) continue;
         const Unit x = unit_of(u, tid == 0);
         if (x.cnt > 0 || !x.live) continue;
         const size_t o = (size_t)x.b * a.f * a.hq + (size_t)x.h * a.g;  // sparse: f = 1
@@ -778,7 +791,7 @@ cudaError_t launch_t(const DecodeQ4Args &a, int ctas, cudaStream_t st) {
     attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
     attr[1].val.cooperative = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    cfg.numAttrs = a.grid_bar != nullptr && ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, NT>, a);
 }
 
@@ -815,12 +828,19 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     a.num_pages = s.num_pages;
     a.bs = s.bs;
     a.scale_log2 = s.sm_scale * 1.4426950408889634f;
+    const int rows = block_idx ? s.g : f * s.g;
     // one CTA per SM (two partial slots a CTA in the decode partials), no more than the
     // longest lists could use
     const long long most = (long long)s.batch * s.hkv * (block_idx ? (long long)max_topk + 1 : s.max_pages);
     const long long ctas_most = (most * s.bs + 255) / 256;
-    const int all = sms < kNumSms ? sms : kNumSms, ctas = ctas_most < all ? (int)ctas_most : all;
-    const int rows = block_idx ? s.g : f * s.g;
+    const int all = sms < kNumSms ? sms : kNumSms;
+    int ctas = ctas_most < all ? (int)ctas_most : all;
+    // Units short enough for one CTA each: no barrier, no merge, no cooperative launch.
+    const long long longest = (block_idx ? (long long)max_topk + 1 : s.max_pages) * s.bs;
+    if (longest <= kWholeKeys[rows > 8]) {
+        a.grid_bar = nullptr;
+        ctas = s.batch * s.hkv;
+    }
     if (s.d == 128) return rows <= 8 ? launch_t<128, 1>(a, ctas, st) : launch_t<128, 2>(a, ctas, st);
     return rows <= 8 ? launch_t<64, 1>(a, ctas, st) : launch_t<64, 2>(a, ctas, st);
 }
