@@ -3,13 +3,14 @@
 // rows of one kv head (a group's heads, or the heads of a few chunk rows) read
 // each 4-bit key and value once.
 //
-// Work.  A unit is a (sequence, kv head) with its list of blocks.  The blocks
-// of all units form one line of W entries, and CTA c of G takes entries
-// [cW/G, (c+1)W/G): every CTA gets the same share whatever the lengths, and its
-// share is a run of pieces, each one unit's.  A unit inside one CTA is written
-// directly; of a unit that spans several, each CTA stores a partial (o, max,
-// sum) and the last to arrive, counted by a ticket it resets, adds them up in
-// CTA order, so the result does not depend on the arrival order.
+// Work.  A unit is a (sequence, kv head) with its list of blocks.  Short units go
+// to a CTA each.  Else every unit is cut into even shares, one a CTA, or, where
+// that would leave some CTAs with much more than others (many unequal units), the
+// blocks of all units form one line of W entries, and CTA c of G takes entries
+// [cW/G, (c+1)W/G), a run of pieces, each one unit's.  A unit inside one CTA is
+// written directly; of a unit that spans several, each CTA stores a partial (o,
+// max, sum), and behind a grid barrier they add them up, each an equal share of
+// the rows, in CTA order, so the result does not depend on the arrival order.
 //
 // Inside a piece, warp w takes every eighth step of 32 positions (two tiles of
 // 16) through a private cp.async ring of kStages steps and keeps its own
@@ -40,6 +41,10 @@ struct Q4Warps {
 // 2048 keys 16-17 and 16, 17, 24, 4096 keys 26-27 and 12, 20, 33; with 16 heads a group 512
 // keys 11 and 12-13 us, 1024 keys 15 and 13, 13, 24.
 constexpr int kWholeKeys[2] = {2048, 768};
+// With units for most of the SMs: 128 units of 8192 keys 50 us whole and 54 split, 256 units of
+// 1 .. 2500 keys 30 and 57.
+constexpr int kWholeKeysMany = 8192;
+constexpr int kPieceKeys = 2048;   // keys a CTA takes in the time that a second piece adds
 constexpr float kShift = 13.f;     // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 2.f;      // growth of the maximum tolerated before rescaling
 
@@ -147,6 +152,8 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     constexpr int kRows = NT * 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int sh_sum[kWarps], sh_unit, sh_first;
+    __shared__ int2 sh_own;
+    __shared__ int sh_most;  // blocks of the longest unit
     __shared__ int4 sh_units[kThreads];  // (blocks, length, fresh tokens, row) when they fit
     __shared__ float2 sh_ml[kRows];  // a row's maximum and sum
     __shared__ Part sh_part[2];      // this CTA's partial pieces: the first one, a later one
@@ -194,13 +201,35 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     };
 
     if (tid < 2) sh_part[tid].rows = 0;
+    if (tid == 0) sh_most = 0;
     // Whole units (no grid barrier): CTA u takes unit u.  Else prefix sums of the units'
     // blocks: thread t sums units [t * per, ...).
     const bool split = a.grid_bar != nullptr;
     const int per = (units + kThreads - 1) / kThreads;
     const bool kept = per == 1 && split;  // the units' data are in sh_units
     int W = 0, G = 1, x0 = 0, x1 = 0;
+    int own = 0, own_first = 0;  // even shares of each unit: the CTAs of this one's unit, the first of them
     auto entry_of = [&](int q) -> int { return q < G ? (int)((long long)W * q / G) : W; };
+    // Sums over the threads before this one (exclusive) and over all.
+    auto scan = [&](int mine, int &all) -> int {
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) sh_sum[warp] = incl;
+        __syncthreads();
+        all = 0;
+        int before = incl - mine;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sh_sum[w];
+            all += sh_sum[w];
+        }
+        return before;
+    };
     if (split) {
         const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
         int mine = 0;
@@ -209,41 +238,59 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             mine += x.cnt;
             if (kept) sh_units[u] = make_int4(x.cnt, x.L, x.n, x.row);
         }
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) sh_sum[warp] = incl;
-        __syncthreads();
-        int before = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sh_sum[w];
-            W += sh_sum[w];
-        }
-        incl += before;
-        // CTAs that take work: enough for a step of every warp each, or one a unit
-        const int least = max(1, 32 * kWarps / a.bs);
-        G = max(1, min(min((int)gridDim.x, W), max(units, (W + least - 1) / least)));
-        // With many CTAs a unit, as many for each: equal units then begin with a CTA's share.
-        if (G >= 8 * units) G -= G % units;
-        x0 = entry_of(cta);
-        x1 = entry_of(cta + 1);
-        if (x0 < x1 && incl - mine <= x0 && x0 < incl) {  // one thread: the unit entry x0 lies in
-            int s = incl - mine;
-            for (int u = u_lo; u < u_hi; ++u) {
-                const int k = kept ? mine : unit_of(u, false).cnt;
-                if (x0 < s + k) {
-                    sh_unit = u;
-                    sh_first = s;
-                    break;
+        const int before = scan(mine, W);
+        if (kept && mine > 0) atomicMax(&sh_most, mine);
+        const int grid = gridDim.x;
+        const int least = max(1, 32 * kWarps / a.bs);  // a step of every warp
+        int share = 0;
+        if (kept && units < grid && W > 0) {
+            // Shares of `share` entries of one unit each, so that every CTA has one piece: the
+            // smallest of five that keeps to the grid (the last one does), unless it is more
+            // than kPieceKeys above the even share, which is what a second piece costs.
+            const int even = (W + grid - 1) / grid, last = (W + grid - units - 1) / (grid - units);
+#pragma unroll 1
+            for (int k = 0; k < 5; ++k) {
+                share = max(least, even + (int)((long long)(last - even) * k / 4));
+                int ctas;
+                const int first = scan((mine + share - 1) / share, ctas);
+                if (ctas > grid) continue;
+                if ((long long)(min(share, sh_most) - max(least, even)) * a.bs > kPieceKeys) share = 0;
+                if (share > 0 && first <= cta && cta < first + (mine + share - 1) / share) {
+                    sh_unit = tid;
+                    sh_first = before;
+                    sh_own = make_int2((mine + share - 1) / share, first);
                 }
-                s += k;
+                if (share > 0 && cta >= ctas && tid == 0) sh_own = make_int2(0, 0);
+                break;
             }
         }
-        __syncthreads();
+        if (share > 0) {
+            __syncthreads();
+            own = sh_own.x;
+            own_first = sh_own.y;
+            if (own > 0) {
+                x0 = sh_first + (cta - own_first) * share;
+                x1 = min(x0 + share, sh_first + sh_units[sh_unit].x);
+            }
+        } else {
+            // the line of entries in even shares
+            G = max(1, min(min(grid, W), max(units, (W + least - 1) / least)));
+            x0 = entry_of(cta);
+            x1 = entry_of(cta + 1);
+            if (x0 < x1 && before <= x0 && x0 < before + mine) {  // one thread: the unit entry x0 lies in
+                int s = before;
+                for (int u = u_lo; u < u_hi; ++u) {
+                    const int k = kept ? mine : unit_of(u, false).cnt;
+                    if (x0 < s + k) {
+                        sh_unit = u;
+                        sh_first = s;
+                        break;
+                    }
+                    s += k;
+                }
+            }
+            __syncthreads();
+        }
     } else {
         x1 = unit_of(cta, false).cnt;
     }
@@ -709,9 +756,9 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             const Part pt = sh_part[w2];
             if (pt.rows == 0) continue;
             // CTAs q0 .. q1 whose shares meet the unit; only q0's can begin before it
-            const int q0 = (int)((((long long)pt.ustart + 1) * G - 1) / W);
-            const int q1 = (int)(((long long)pt.uend * G - 1) / W);
-            const int parts = q1 - q0 + 1, odd = entry_of(q0) < pt.ustart ? 1 : 0;
+            const int q0 = own > 0 ? own_first : (int)((((long long)pt.ustart + 1) * G - 1) / W);
+            const int q1 = own > 0 ? q0 + own - 1 : (int)(((long long)pt.uend * G - 1) / W);
+            const int parts = q1 - q0 + 1, odd = own == 0 && entry_of(q0) < pt.ustart ? 1 : 0;
             const int items = pt.rows * (D / 4);
             const int i0 = items * (cta - q0) / parts, i1 = items * (cta - q0 + 1) / parts;
             const int lg = parts > 16 ? 5 : parts > 8 ? 4 : parts > 4 ? 3 : parts > 2 ? 2 : 1;
@@ -837,9 +884,10 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     int ctas = ctas_most < all ? (int)ctas_most : all;
     // Units short enough for one CTA each: no barrier, no merge, no cooperative launch.
     const long long longest = (block_idx ? (long long)max_topk + 1 : s.max_pages) * s.bs;
-    if (longest <= kWholeKeys[rows > 8]) {
+    const int units = s.batch * s.hkv;
+    if (longest <= kWholeKeys[rows > 8] || (longest <= kWholeKeysMany && units * 5 >= all * 4)) {
         a.grid_bar = nullptr;
-        ctas = s.batch * s.hkv;
+        ctas = units;
     }
     if (s.d == 128) return rows <= 8 ? launch_t<128, 1>(a, ctas, st) : launch_t<128, 2>(a, ctas, st);
     return rows <= 8 ? launch_t<64, 1>(a, ctas, st) : launch_t<64, 2>(a, ctas, st);
