@@ -95,9 +95,10 @@ def attention_tolerance(mag, n, a, vsum=0.0):
     unit, which may drop bits below 2^-22 of the running magnitude at each of 8 steps, and the
     scaling rounds twice more: at most 10 * 2^-22 of sum |q k| = mag.  Weights: e^(2 delta) - 1,
     2^-21 for the exponential, 2^-21 for the two fp16 halves, whose absolute rounding is half of
-    fp16's smallest step, 2^-25, where the row's largest weight is at least 2^12: 2^-37 of |v|
-    for every key.  Sums over n weights: one addition
+    fp16's smallest step, 2^-25, where the row's largest weight is at least 2^11 (weights are
+    scaled by 2^13 with 2 powers of slack in the maximum, or by 2^12 with 3, less one for the
+    maximum's rounding up: 2^(12 - 1)): 2^-36 of |v| for every key.  Sums over n weights: one addition
     a 16-position step, split over at least 1 warp, 2^-22 each, and 64 more for the merges."""
     delta = 10 * 2.0 ** -22 * mag
     sums = (n / 16 + 64) * 2.0 ** -22
-    return a * (2 * delta + 2.0 ** -20 + 2 * sums) + 2.0 ** -37 * vsum + 1e-30, delta + 2.0 ** -20 + sums
+    return a * (2 * delta + 2.0 ** -20 + 2 * sums) + 2.0 ** -36 * vsum + 1e-30, delta + 2.0 ** -20 + sums
