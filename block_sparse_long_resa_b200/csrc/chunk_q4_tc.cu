@@ -11,40 +11,40 @@
 // bounded grid barrier (cooperative launch, one CTA per SM) those CTAs merge an
 // equal share of its rows, in CTA order.
 //
-// Warp roles (768 threads; registers moved from the others to the softmax warps):
-//   warps 0-3    expand the 4-bit tiles, c * s in fp16 (exact), into 128-byte
-//                swizzled operand tiles: a ring of three 32 KB slots K0 V0 K1 V1 ..;
-//   warps 4-19   softmax: eight warps an M tile, two threads a row, each with 64 of
-//                the tile's keys and half of O's channels; they tell each other
-//                the maximum;
-//   warp 20      TMEM owner and MMA issuer;
-//   warps 21-22  bring the 4-bit tiles in (cp.async), two tiles ahead.
+// Warp roles (384 threads; registers moved from warpgroup 0 to the others):
+//   warp 0      TMEM owner and MMA issuer (one thread);
+//   warps 1-3   bring the 4-bit tiles in (cp.async, three raw stages) and expand
+//               them, c * s in fp16 (exact), into 128-byte swizzled operand tiles:
+//               a ring of three 32 KB slots K0 V0 K1 V1 ..;
+//   warps 4-7, 8-11   softmax of M tile 0 and 1, one thread a row.
 // Per M tile the chain is QK^T(i) -> softmax -> P V(i) -> QK^T(i+1); the two M
 // tiles run half a period apart, so one's MMAs fill the other's softmax.
 //
 // Precision.  q enters as fp16 scaled per row by a power of two (its 8 bits stay
 // exact), so Q K^T has exact products.  P enters as fp16 hi + lo (22 bits), both
-// over the tile's S in tensor memory, 16 keys (8 + 8 columns) at a time.  The
+// over the tile's S in tensor memory, 32 keys (16 + 16 columns) at a time.  The
 // matrix unit truncates when it adds to its fp32 accumulator, which over a long
-// sequence would be a bias of 10^-5, so O starts from zero every kChain tiles and
-// is added to the row in memory, where additions round to nearest.
+// sequence would be a bias of 10^-5, so P V starts from zero at every tile and
+// the softmax thread adds the tile's O to its row in registers (fused with the
+// rescaling, o = o * 2^(m - m') + tile), where additions round to nearest.
 #include "q4_common.cuh"
 #include "tc_common.cuh"
 
 namespace resa {
 namespace {
 
-constexpr int kThreads = 768;
+constexpr int kThreads = 384;
 constexpr int kRows = kRectRowsPerCta;  // 256
 constexpr int kKeys = 128;              // keys per tile
 constexpr int kSlots = 3;               // fp16 operand tiles
 constexpr int kRaw = 3;                 // 4-bit tiles in flight
-constexpr int kConvWarps = 4, kSoftmaxWarp = 4, kMmaWarp = 20, kLoadWarp = 21, kLoadWarps = 2;
-constexpr int kLaunchRegs = 80;         // 768 threads: the whole file
-constexpr int kConvRegs = 72, kSoftmaxRegs = 88, kOtherRegs = 56;
-static_assert(kConvRegs + 4 * kSoftmaxRegs + kOtherRegs <= 6 * kLaunchRegs, "registers of the launch");
-constexpr int kChain = 16;              // tiles whose P V add up in tensor memory
+constexpr int kConv = 96;               // converter threads
+constexpr int kLaunchRegs = 168;        // 384 threads: 64512 of the file's 65536
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers of the launch");
+constexpr int kPieceTiles = 8;          // tiles a CTA takes in the time that a second piece adds
 constexpr int kMinTiles = 2;            // tiles a CTA takes at least, when there are few
+constexpr int kChain = 4;               // tiles whose P V add up in tensor memory
 constexpr float kShift = 12.f;          // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 3.f;           // growth of the maximum tolerated before rescaling
 
@@ -205,83 +205,120 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
-    __shared__ uint64_t q_ready[2], slot_full[kSlots], slot_free[kSlots], s_full[2], p_full[2];
+    __shared__ uint64_t q_ready[2], slot_full[kSlots], slot_free[kSlots], s_full[2], p_full[2][2];
     __shared__ uint32_t tmem_base_s, sh_ok;
     __shared__ uint64_t raw_full[kRaw], raw_free[kRaw];
-    __shared__ uint32_t raw_mask[kRaw];  // a raw tile's valid blocks
     __shared__ uint32_t tile_mask[4];    // a tile's valid runs of 16 keys
-    __shared__ uint64_t pair_bar[8];     // the two warps of 32 rows
-    __shared__ float sh_x[2][2][2][128]; // what they tell each other, two messages deep
-    __shared__ int sh_sum[kThreads / 32], sh_w, sh_ctas, sh_first, sh_unit;
+    __shared__ int sh_sum[kThreads / 32], sh_w, sh_ctas, sh_first, sh_unit, sh_x[2], sh_most;
+    __shared__ int2 sh_own;  // even shares: the CTAs of this one's unit, the first of them
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units = a.batch * a.hkv * a.groups;
     const int cta = blockIdx.x;
 
-    // This CTA's share of the line: prefix sums of the units' tiles.
+    // This CTA's share of the units' tiles (as in the split-KV kernel): an even share of one
+    // unit, so that every CTA has one piece, or, where that would give some CTAs kPieceTiles
+    // more than others, a share of the line of all tiles.
     const int per = (units + kThreads - 1) / kThreads;
     const int u_lo = min(units, tid * per), u_hi = min(units, u_lo + per);
     int mine = 0;
     for (int u = u_lo; u < u_hi; ++u) mine += chunk_unit(a, u, nullptr).cnt;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sh_sum[warp] = incl;
     if (tid == 0) {
+        sh_most = 0;
+        sh_own = make_int2(0, 0);
+        sh_x[0] = sh_x[1] = 0;
         for (int s = 0; s < kRaw; ++s) {
-            mbar_init(&raw_full[s], 32 * kLoadWarps + 1);
-            mbar_init(&raw_free[s], kConvWarps);
+            mbar_init(&raw_full[s], kConv);
+            mbar_init(&raw_free[s], 3);
         }
         for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&slot_full[s], 32 * kConvWarps);
+            mbar_init(&slot_full[s], kConv);
             mbar_init(&slot_free[s], 1);
         }
         for (int m = 0; m < 2; ++m) {
-            mbar_init(&q_ready[m], 256);
+            mbar_init(&q_ready[m], 128);
             mbar_init(&s_full[m], 1);
-            mbar_init(&p_full[m], 256);
+            mbar_init(&p_full[m][0], 128);
+            mbar_init(&p_full[m][1], 128);
         }
-        for (int x = 0; x < 8; ++x) mbar_init(&pair_bar[x], 64);
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base_s, 512);
+    if (warp == 0) tc::tmem_alloc(&tmem_base_s, 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = tmem_base_s;
     {
-        int W = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) incl += sh_sum[w];
-            W += sh_sum[w];
+        // sums over the threads before this one and over all
+        auto scan = [&](int x, int &all) -> int {
+            int incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            __syncthreads();
+            if (lane == 31) sh_sum[warp] = incl;
+            __syncthreads();
+            all = 0;
+            int before = incl - x;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) before += sh_sum[w];
+                all += sh_sum[w];
+            }
+            return before;
+        };
+        int W;
+        const int before = scan(mine, W), grid = gridDim.x;
+        int share = 0;
+        if (per == 1 && units < grid && W > 0) {
+            if (mine > 0) atomicMax(&sh_most, mine);
+            const int even = (W + grid - 1) / grid, last = (W + grid - units - 1) / (grid - units);
+#pragma unroll 1
+            for (int k = 0; k < 5; ++k) {  // the smallest of five shares that keep to the grid
+                share = max(kMinTiles, even + (int)((long long)(last - even) * k / 4));
+                int ctas;
+                const int mine_ctas = (mine + share - 1) / share, first = scan(mine_ctas, ctas);
+                if (ctas > grid) continue;
+                if (min(share, sh_most) - max(kMinTiles, even) > kPieceTiles) share = 0;
+                if (share > 0 && first <= cta && cta < first + mine_ctas) {
+                    sh_unit = tid;
+                    sh_first = before;
+                    sh_own = make_int2(mine_ctas, first);
+                    sh_x[0] = before + (cta - first) * share;
+                    sh_x[1] = min(sh_x[0] + share, before + mine);
+                }
+                break;
+            }
         }
-        const int G = max(1, min((int)gridDim.x, (W + kMinTiles - 1) / kMinTiles));
+        const int G = max(1, min(grid, (W + kMinTiles - 1) / kMinTiles));
         if (tid == 0) {
             sh_w = W;
             sh_ctas = G;
         }
-        const int x0 = entry_of(cta, W, G);
-        if (x0 < entry_of(cta + 1, W, G) && incl - mine <= x0 && x0 < incl) {
-            int s = incl - mine;
-            for (int u = u_lo; u < u_hi; ++u) {
-                const int k = chunk_unit(a, u, nullptr).cnt;
-                if (x0 < s + k) {
-                    sh_unit = u;
-                    sh_first = s;
-                    break;
+        if (share == 0) {
+            const int x0 = entry_of(cta, W, G), x1 = entry_of(cta + 1, W, G);
+            if (x0 < x1 && before <= x0 && x0 < before + mine) {  // one thread: the unit that x0 lies in
+                int s = before;
+                for (int u = u_lo; u < u_hi; ++u) {
+                    const int k = chunk_unit(a, u, nullptr).cnt;
+                    if (x0 < s + k) {
+                        sh_unit = u;
+                        sh_first = s;
+                        sh_x[0] = x0;
+                        sh_x[1] = x1;
+                        break;
+                    }
+                    s += k;
                 }
-                s += k;
             }
         }
     }
     __syncthreads();
     auto start = [&]() -> Walk {
         Walk w;
-        w.x = entry_of(cta, sh_w, sh_ctas);
-        w.x1 = entry_of(cta + 1, sh_w, sh_ctas);
+        w.x = sh_x[0];
+        w.x1 = sh_x[1];
         w.u = w.x < w.x1 ? sh_unit : 0;
         w.ustart = w.x < w.x1 ? sh_first : 0;
         w.slot = 0;
@@ -293,173 +330,82 @@ __global__ void __launch_bounds__(kThreads, 1)
     Piece p;
 
     // Registers move from the other warps to the softmax warps and back at the end.
-    if (warp < 4) {  // ----------------------------------------------------- converters
-        set_regs<kConvRegs, false>();
-        const int bs_shift = a.bs == 64 ? 6 : a.bs == 32 ? 5 : 4;
-        const uint32_t raw_s = smem_u32(smem + SM::kRawOff), slots_s = smem_u32(slots);
-        // A lane converts the 16-byte chunk c (32 channels) of row r1 of every step of
-        // 32 chunks.  Lanes of the upper channel half take their words in the order
-        // 2 3 0 1, so that the eight lanes of a store phase meet all banks.
-        constexpr int kPerRow = D / 32, kStepRows = 32 / kPerRow;
-        const int r1 = lane / kPerRow, c = lane % kPerRow;
-        const bool swap = c >= 2;
-        const uint32_t x0 = (uint32_t)((((c & 1) * 4) ^ (swap ? 2 : 0) ^ (r1 & 7)) << 4);
-        uint32_t j = 0, tiles = 0;
-        bool ok = true;
-        for (Walk w = start(); ok && w.next(a, p);) {
-            for (int t = p.t0; t < p.t1; ++t, ++tiles) {
-                const uint32_t st = tiles % kRaw;
-                ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&raw_full[st], (tiles / kRaw) & 1));
-                if (!ok) break;
-                const uint32_t mask = raw_mask[st];
-                const int left = p.L - t * kKeys;  // rows of the tile below the length
-                const bool whole_tile = left >= kKeys && mask == (1u << (kKeys >> bs_shift)) - 1u;
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++j) {
-                    const uint32_t code_at = raw_s + st * SM::kRawStage + kv * SM::kCodes + lane * 16;
-                    const uint32_t scale_at = raw_s + st * SM::kRawStage + 2 * SM::kCodes + kv * SM::kScales +
-                                              lane * 2;
-                    const uint32_t dst = slots_s + (j % kSlots) * SM::kTile + (c / 2) * SM::kHalf + r1 * 128 + x0;
-                    constexpr int kSteps = kKeys / kStepRows / kConvWarps;
-                    uint32_t xs[kSteps][4];
-                    uint16_t sf[kSteps];
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const int step = warp + kConvWarps * k;
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(xs[k][0]), "=r"(xs[k][1]), "=r"(xs[k][2]), "=r"(xs[k][3])
-                                     : "r"(code_at + step * 512));
-                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sf[k]) : "r"(scale_at + step * 64));
-                    }
-                    if (j >= kSlots)
-                        ok = ok && mbar_wait_bounded(&slot_free[j % kSlots], ((j / kSlots) - 1) & 1);
-                    if (kv == 0 && tid == 0) {
-                        uint32_t m16 = 0;
-                        for (int x = 0; x < kKeys / 16; ++x)
-                            m16 |= ((mask >> ((x * 16) >> bs_shift)) & 1u) << x;
-                        tile_mask[tiles & 3] = m16;
-                    }
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        const int step = warp + kConvWarps * k;
-                        if (!whole_tile) {
-                            const int r = step * kStepRows + r1;
-                            if (r >= left || !((mask >> (r >> bs_shift)) & 1u)) sf[k] = 0;  // counts as 0
-                        }
-                        const uint32_t s2 = e4m3x2_to_f16(sf[k]);
-                        const uint32_t sw[2] = {__byte_perm(s2, s2, swap ? 0x3232 : 0x1010),
-                                                __byte_perm(s2, s2, swap ? 0x1010 : 0x3232)};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t y[4];
-                            e2m1x8_to_f16(swap ? xs[k][i ^ 2] : xs[k][i], y);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) y[z] = mul_f16x2(y[z], sw[i / 2]);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                             (dst + step * (kStepRows * 128)) ^ (i << 4)),
-                                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                                         : "memory");
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&slot_full[j % kSlots]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&raw_free[st]);
-            }
-        }
-        if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
-        __syncwarp();
-        set_regs<kLaunchRegs, true>();
-    } else if (warp < kMmaWarp) {  // ------------------------------------------ softmax
+    if (warp >= 4) {  // ------------------------------------------------------- softmax
         set_regs<kSoftmaxRegs, true>();
-        const int m = (warp - kSoftmaxWarp) >> 3, hf = ((warp - kSoftmaxWarp) >> 2) & 1;
-        const int r = 32 * (warp & 3) + lane;
+        const int m = (warp - 4) >> 2, r = (tid - 128) & 127;
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t scol = tmem + lane_base + m * kKeys;
-        constexpr int kCh = D / 2;  // channels of O a thread keeps
-        const uint32_t ocol = tmem + lane_base + 2 * kKeys + m * D + hf * kCh;
-        uint32_t ns = 0, nx = 0, tiles = 0;  // S tiles (and last P V) seen, messages, key tiles so far
+        const uint32_t ocol = tmem + lane_base + 2 * kKeys + m * D;
+        uint32_t ns = 0, tiles = 0;  // S tiles (and last P V) seen, key tiles so far
         bool ok = true;
-        // This thread's x to the other thread of its row, and that one's.
-        auto exchange = [&](float x) -> float {
-            sh_x[nx & 1][m][hf][r] = x;
-            uint64_t *bar = &pair_bar[m * 4 + (warp & 3)];
-            mbar_arrive(bar);
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, nx & 1));
-            return sh_x[nx++ & 1][m][hf ^ 1][r];
-        };
         for (Walk w = start(); w.next(a, p); tiles += (uint32_t)(p.t1 - p.t0)) {
             const int T = p.t1 - p.t0, nm = p.rows > 128 ? 2 : 1;
-            if (m >= nm) continue;
             const int lrow = m * 128 + r, rho = p.row0 + lrow;
             const bool row_ok = lrow < p.rows;
-            const int lim = row_ok ? p.L - p.n + rho / a.g + 1 : 0;     // keys the row sees
-            const int lim_warp = p.L - p.n + (rho - lane) / a.g + 1;     // keys every row of the warp sees
-            // Q row, scaled to [2^8, 2^9) at its largest, into the swizzled tile
+            const int pos_first = p.L - p.n;
+            const int lim = row_ok ? pos_first + rho / a.g + 1 : 0;  // keys the row sees
+            const int lim_warp = pos_first + (rho - lane) / a.g + 1;  // keys every row of the warp sees
+            const size_t orow = ((size_t)p.b * a.f + rho / a.g) * hq + (size_t)p.h * a.g + rho % a.g;
+            // The warp's 32 Q rows, each scaled to [2^8, 2^9) at its largest, into the swizzled
+            // tile: D / 8 lanes a row, so that its loads are runs.
             int e = 0;
-            {
-                const size_t orow = ((size_t)p.b * a.f + rho / a.g) * hq + (size_t)p.h * a.g + rho % a.g;
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + orow * D);
-                uint32_t mag = 0;
-                if (row_ok) {
-#pragma unroll 4
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 x = src[c];
-                        mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-                    }
-                    mag = max(mag & 0xffffu, mag >> 16);
-                    // zero and non-finite rows keep factor 1
-                    if (mag != 0 && mag < 0x7f80u) e = max(-110, min(119, (int)(mag >> 7) - 127 - 8));
+            if (m < nm) {
+                constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
+                const int sub = lane / kLanes, c = lane % kLanes;
+uint4 xs[kLanes];  // all loads before the first use: one trip to memory
+#pragma unroll
+                for (int it = 0; it < kLanes; ++it) {
+                    const int qrow = m * 128 + (r - lane) + it * kRowsAt + sub, qrho = p.row0 + qrow;
+                    xs[it] = make_uint4(0u, 0u, 0u, 0u);
+                    if (qrow < p.rows)
+                        xs[it] = reinterpret_cast<const uint4 *>(
+                            a.q + (((size_t)p.b * a.f + qrho / a.g) * hq + (size_t)p.h * a.g + qrho % a.g) * D)[c];
                 }
-                const float f2 = pow2i(-e);
-#pragma unroll 4
-                for (int c = hf * (D / 16); c < (hf + 1) * (D / 16); ++c) {
-                    const uint4 x = row_ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int it = 0; it < kLanes; ++it) {
+                    const uint4 x = xs[it];
+                    const int qr = (r - lane) + it * kRowsAt + sub;
+                    uint32_t mag = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                            __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+                    mag = max(mag & 0xffffu, mag >> 16);
+#pragma unroll
+                    for (int o = kLanes / 2; o > 0; o >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+                    // zero and non-finite rows keep factor 1
+                    int ee = 0;
+                    if (mag != 0 && mag < 0x7f80u) ee = max(-110, min(119, (int)(mag >> 7) - 127 - 8));
+                    const float f2 = pow2i(-ee);
                     const uint4 y = make_uint4(pack_f16(bf_lo(x.x) * f2, bf_hi(x.x) * f2),
                                                pack_f16(bf_lo(x.y) * f2, bf_hi(x.y) * f2),
                                                pack_f16(bf_lo(x.z) * f2, bf_hi(x.z) * f2),
                                                pack_f16(bf_lo(x.w) * f2, bf_hi(x.w) * f2));
-                    *reinterpret_cast<uint4 *>(smem + m * SM::kTile + (c / 8) * SM::kHalf +
-                                               swz128(r, c % 8)) = y;
+                    *reinterpret_cast<uint4 *>(smem + m * SM::kTile + (c / 8) * SM::kHalf + swz128(qr, c % 8)) = y;
+                    const int mine = __shfl_sync(0xffffffffu, ee, lane % kRowsAt * kLanes);
+                    if (lane / kRowsAt == it) e = mine;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&q_ready[m]);
             }
+            if (m >= nm) continue;
             const float rs = a.scale_log2 * head_scale(a.c.k_scale, p.h) * pow2i(e);
-            float mx = -INFINITY, l = 0.f;
-            // The row's O outside tensor memory, relative to 2^mo: in the CTA's partial slot,
-            // [32-row group][channel / 4][row in group][4], so that a warp's accesses are runs.
-            float4 *row_o = reinterpret_cast<float4 *>(a.part_o + (size_t)(2 * cta + p.slot) * kRows * D) +
-                            ((size_t)(lrow / 32) * (D / 4) + hf * (kCh / 4)) * 32 + lane;
-            float mo = -INFINITY;
-            // Add the kChain tiles' O to it (relative to 2^mx).
-            auto flush = [&](bool fresh) {
-                const float f2 = mo == mx || mo == -INFINITY ? 1.f : ex2(mo - mx);
-#pragma unroll 1
-                for (int c = 0; c < kCh; c += 16) {
-                    uint32_t ov[16];
-                    tc::tmem_ld16(ocol + c, ov);
-                    tc::tmem_wait_ld();
-                    if (!row_ok) continue;
+            float mx = -INFINITY, l = 0.f, mo = -INFINITY;  // acc is relative to 2^mo
+            uint64_t acc[D / 2];  // pairs of channels
 #pragma unroll
-                    for (int x = 0; x < 16; x += 4) {
-                        float4 v = make_float4(__uint_as_float(ov[x]), __uint_as_float(ov[x + 1]),
-                                               __uint_as_float(ov[x + 2]), __uint_as_float(ov[x + 3]));
-                        float4 *dst = row_o + (c + x) / 4 * 32;
-                        if (fresh) {
-                            __stcg(dst, v);
-                        } else if (f2 == 1.f) {
-                            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst),
-                                         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                                         : "memory");
-                        } else {
-                            const float4 u = __ldcg(dst);
-                            __stcg(dst, make_float4(fmaf(u.x, f2, v.x), fmaf(u.y, f2, v.y),
-                                                    fmaf(u.z, f2, v.z), fmaf(u.w, f2, v.w)));
-                        }
-                    }
+            for (int c = 0; c < D / 2; ++c) acc[c] = 0ull;
+            // Add the O in tensor memory (relative to 2^mx).
+            auto drain = [&]() {
+                const float f = mo == mx || mo == -INFINITY ? 1.f : ex2(mo - mx);
+                const uint64_t f2 = pack2(f, f);
+                uint32_t ov[2][16];
+                tc::tmem_ld16(ocol, ov[0]);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    tc::tmem_wait_ld();
+                    if (c + 1 < D / 16) tc::tmem_ld16(ocol + 16 * (c + 1), ov[(c + 1) & 1]);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        acc[8 * c + x] = fma2(acc[8 * c + x], f2,
+                                              pack2(__uint_as_float(ov[c & 1][2 * x]),
+                                                    __uint_as_float(ov[c & 1][2 * x + 1])));
                 }
                 mo = mx;
             };
@@ -474,23 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the row's largest logit
                 float mt = -INFINITY, mt2 = -INFINITY;
                 if (full) {
-                    uint32_t sv[2][32];
-                    tc::tmem_ld32(scol + 64 * hf, sv[0]);
-                    tc::tmem_wait_ld();
-                    tc::tmem_ld32(scol + 64 * hf + 32, sv[1]);
+                    uint32_t sv[2][16];
+                    tc::tmem_ld16(scol, sv[0]);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (c == 1) tc::tmem_wait_ld();
+                    for (int c = 0; c < kKeys / 16; ++c) {
+                        tc::tmem_wait_ld();
+                        if (c + 1 < kKeys / 16) tc::tmem_ld16(scol + 16 * (c + 1), sv[(c + 1) & 1]);
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            mt = max3(mt, __uint_as_float(sv[c][x]), __uint_as_float(sv[c][x + 1]));
-                            mt2 = max3(mt2, __uint_as_float(sv[c][x + 2]), __uint_as_float(sv[c][x + 3]));
+                        for (int x = 0; x < 16; x += 4) {
+                            mt = max3(mt, __uint_as_float(sv[c & 1][x]), __uint_as_float(sv[c & 1][x + 1]));
+                            mt2 = max3(mt2, __uint_as_float(sv[c & 1][x + 2]), __uint_as_float(sv[c & 1][x + 3]));
                         }
                     }
                     mt = fmaxf(mt, mt2);
                 } else {
 #pragma unroll 1
-                    for (int c = 4 * hf; c < 4 * hf + 4; ++c) {
+                    for (int c = 0; c < kKeys / 16; ++c) {
                         uint32_t sv[16];
                         tc::tmem_ld16(scol + 16 * c, sv);
                         tc::tmem_wait_ld();
@@ -500,10 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (x < left) mt = fmaxf(mt, __uint_as_float(sv[x]));
                     }
                 }
-                mt = fmaxf(mt, exchange(mt)) * rs;
-                if (!ok) break;
-                // O of the last kChain tiles leaves tensor memory before P V overwrites it
-                if (i > 0 && i % kChain == 0) flush(i == kChain);
+                mt *= rs;
+                // O of the last kChain tiles joins the row before P V overwrites it
+                if (i > 0 && i % kChain == 0) drain();
                 // The maximum moves (to a whole number, so that every factor 2^(m - m') is
                 // exact) only when it grows by more than kSlack; rarely after the first tiles.
                 const bool grow = mt > mx + kSlack;
@@ -514,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= al;
                     if (i % kChain != 0) {
 #pragma unroll 1
-                        for (int c = 0; c < kCh; c += 16) {
+                        for (int c = 0; c < D; c += 16) {
                             uint32_t ov[16];
                             tc::tmem_ld16(ocol + c, ov);
                             tc::tmem_wait_ld();
@@ -528,41 +472,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t rs2 = pack2(rs, rs), nb2 = pack2(nb, nb), minus = pack2(-1.f, -1.f);
                 uint64_t ls[2] = {0ull, 0ull};
                 uint32_t sv[2][16];
-                tc::tmem_ld16(scol + 64 * hf, sv[0]);
+                tc::tmem_ld16(scol, sv[0]);
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t col = scol + 64 * hf + 16 * c;
-                    uint32_t (&x)[16] = sv[c & 1];
-                    tc::tmem_wait_ld();
-                    if (c < 3) tc::tmem_ld16(col + 16, sv[(c + 1) & 1]);
-                    if (!full) {
-                        const int left = ((tm >> (4 * hf + c)) & 1u) ? lim - t0 - 64 * hf - 16 * c : 0;
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t col = scol + 64 * hf + 16 * c;
+                        uint32_t (&x)[16] = sv[c & 1];
+                        tc::tmem_wait_ld();
+                        if (c < 3 || hf == 0) tc::tmem_ld16(col + 16, sv[(c + 1) & 1]);
+                        if (!full) {
+                            const int left = ((tm >> (4 * hf + c)) & 1u) ? lim - t0 - 64 * hf - 16 * c : 0;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (k >= left) x[k] = 0xff800000u;
+                            for (int k = 0; k < 16; ++k)
+                                if (k >= left) x[k] = 0xff800000u;
+                        }
+                        uint32_t pw[16];  // 8 columns of hi, 8 of lo
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float p0, p1, l0, l1;
+                            unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), rs2, nb2),
+                                    p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            const uint64_t pp = pack2(p0, p1);
+                            ls[k & 1] = add2(ls[k & 1], pp);
+                            // hi: the leading 11 bits, so that lo = p - hi is exact
+                            const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
+                            const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
+                            unpack2(fma2(pack2(h0, h1), minus, pp), l0, l1);
+                            pw[k] = pack_f16(h0, h1);
+                            pw[8 + k] = pack_f16(l0, l1);
+                        }
+                        tc::tmem_st16(col, pw);
                     }
-                    uint32_t pw[16];  // 8 columns of hi, 8 of lo
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        float p0, p1, l0, l1;
-                        unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), rs2, nb2),
-                                p0, p1);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        const uint64_t pp = pack2(p0, p1);
-                        ls[k & 1] = add2(ls[k & 1], pp);
-                        // hi: the leading 11 bits, so that lo = p - hi is exact
-                        const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
-                        const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
-                        unpack2(fma2(pack2(h0, h1), minus, pp), l0, l1);
-                        pw[k] = pack_f16(h0, h1);
-                        pw[8 + k] = pack_f16(l0, l1);
-                    }
-                    tc::tmem_st16(col, pw);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(&p_full[m][hf]);
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(&p_full[m]);
                 {
                     float l0, l1;
                     unpack2(add2(ls[0], ls[1]), l0, l1);
@@ -573,37 +520,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::fence_after_sync();
-            // the row's sum over both halves of the keys, in one order
-            const float lx = exchange(l);
-            if (!ok) break;
-            l = hf == 0 ? l + lx : lx + l;
-            const bool whole = p.t0 == 0 && p.t1 == p.cnt, kept = T > kChain;
-            const float inv = !whole ? 1.f : l == 0.f ? 0.f : head_scale(a.c.v_scale, p.h) / l;
-            const float f2 = !kept || mo == -INFINITY ? 0.f : ex2(mo - mx);
-            const size_t orow = ((size_t)p.b * a.f + rho / a.g) * hq + (size_t)p.h * a.g + rho % a.g;
-            float4 *dst = whole ? reinterpret_cast<float4 *>(a.out + orow * D + hf * kCh) : row_o;
+            drain();
+            const bool whole = p.t0 == 0 && p.t1 == p.cnt;
+            const float inv = l > 0.f ? head_scale(a.c.v_scale, p.h) / l : (l == 0.f ? 0.f : l);
+            const size_t slot = (size_t)(2 * cta + p.slot) * kRows + lrow;
+            // a partial lies as [32-row group][channel / 4][row in group][4], so that a warp's
+            // stores are runs
+            float4 *dst = whole ? reinterpret_cast<float4 *>(a.out + orow * D)
+                                : reinterpret_cast<float4 *>(a.part_o + (size_t)(2 * cta + p.slot) * kRows * D) +
+                                      (size_t)(lrow / 32) * (D / 4) * 32 + lane;
             const int step = whole ? 1 : 32;
-#pragma unroll 1
-            for (int c = 0; c < kCh; c += 16) {
-                uint32_t ov[16];
-                tc::tmem_ld16(ocol + c, ov);
-                tc::tmem_wait_ld();
-                if (!row_ok) continue;
+            if (row_ok) {
+                const uint64_t f2 = whole ? pack2(inv, inv) : pack2(1.f, 1.f);
 #pragma unroll
-                for (int x = 0; x < 16; x += 4) {
-                    float4 v = make_float4(__uint_as_float(ov[x]), __uint_as_float(ov[x + 1]),
-                                           __uint_as_float(ov[x + 2]), __uint_as_float(ov[x + 3]));
-                    if (kept) {
-                        const float4 u = __ldcg(row_o + (c + x) / 4 * 32);
-                        v = make_float4(fmaf(u.x, f2, v.x), fmaf(u.y, f2, v.y), fmaf(u.z, f2, v.z),
-                                        fmaf(u.w, f2, v.w));
-                    }
-                    dst[(c + x) / 4 * step] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                for (int c = 0; c < D / 4; ++c) {
+                    float4 v;
+                    unpack2(fma2(acc[2 * c], f2, 0ull), v.x, v.y);
+                    unpack2(fma2(acc[2 * c + 1], f2, 0ull), v.z, v.w);
+                    dst[c * step] = v;
                 }
             }
-            if (row_ok && hf == 0) {
+            if (row_ok) {
                 if (!whole)
-                    a.part_ml[(size_t)(2 * cta + p.slot) * kRows + lrow] = make_float2(mx, l);
+                    a.part_ml[slot] = make_float2(mx, l);
                 else if (a.lse)
                     a.lse[orow] = l > 0.f ? (mx - kShift + log2f(l)) * 0.6931471805599453f
                                   : l == 0.f ? -INFINITY : l;
@@ -614,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         set_regs<kLaunchRegs, false>();
     } else {
         set_regs<kOtherRegs, false>();
-        if (warp == kMmaWarp) {  // ----------------------------------------------- MMA issuer
+        if (warp == 0) {  // -------------------------------------------- MMA issuer
             // The whole warp runs the loop and one elected thread issues: with the
             // addresses uniform over the warp an MMA issues in its 64 cycles, from
             // a branch of one thread it took 120.
@@ -640,15 +579,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            // O of M tile m from its P and operand tile jj; fresh: the first of kChain tiles
-            auto pv = [&](int m, uint32_t jj, bool fresh) {
-                const uint64_t vd = tc::smem_desc(smem_u32(slots) + (jj % kSlots) * SM::kTile, SM::kHalf, 1024);
+            // O of M tile m from the P and V of keys 64 hf ..; fresh: the first of kChain tiles
+            auto pv = [&](int m, uint32_t jj, int hf, bool fresh) {
+                const uint64_t vd = tc::smem_desc(smem_u32(slots) + (jj % kSlots) * SM::kTile, SM::kHalf, 1024) +
+                                    hf * (SM::kHalf >> 5);
                 if (el) {
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk) {
+                    for (int kk = 0; kk < 4; ++kk) {
                         const uint64_t bd = vd + kk * (16 * 128 >> 4);
-                        const uint32_t pt = tmem + m * kKeys + kk * 16;
-                        tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt, bd, idesc_pv, kk > 0 || !fresh ? 1u : 0u);
+                        const uint32_t pt = tmem + m * kKeys + hf * 64 + kk * 16;
+                        tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt, bd, idesc_pv,
+                                       hf > 0 || kk > 0 || !fresh ? 1u : 0u);
                         tc::mma_f16_ts(tmem + 2 * kKeys + m * D, pt + 8, bd, idesc_pv, 1u);
                     }
                 }
@@ -676,9 +617,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         if (m >= nm || !ok) break;
-                        wait(&p_full[m], np[m]++ & 1);
+                        // half a tile at a time, while the softmax makes the other half
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            wait(&p_full[m][hf], np[m] & 1);
+                            if (ok) pv(m, jv, hf, i % kChain == 0);
+                        }
                         if (!ok) break;
-                        pv(m, jv, i % kChain == 0);
+                        ++np[m];
                         if (m == nm - 1) commit(&slot_free[jv % kSlots]);
                         if (more) {
                             if (m == 0) wait_slot(jk);
@@ -692,32 +638,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
             __syncwarp();
-        } else {  // -------------------------------------------------------- loaders
-            // Runs of 16 keys are contiguous in the cache: one warp takes the even and one the
-            // odd ones of a tile, a lane 16 bytes at a time.  (Bulk copies, one a run
-            // and array, took 80 cycles each to issue.)
-            const int lw = warp - kLoadWarp;
+        } else {  // ------------------------------------------------------ converters
+            // The 4-bit tiles come in two tiles ahead, by runs of 16 keys (contiguous in the
+            // cache): warp w takes runs w - 1, w + 2, .., a lane 16 bytes at a time.  (Bulk
+            // copies, one a run and array, took 80 cycles each to issue.)
             const int bs_shift = a.bs == 64 ? 6 : a.bs == 32 ? 5 : 4;
             const int bpt = kKeys >> bs_shift;  // blocks a tile
-            const uint32_t raw_s = smem_u32(smem + SM::kRawOff);
-            uint32_t tiles = 0;
-            bool ok = lw < kLoadWarps;
-            for (Walk w = start(); ok && w.next(a, p);) {
+            const uint32_t raw_s = smem_u32(smem + SM::kRawOff), slots_s = smem_u32(slots);
+            // A lane converts the 16-byte chunk c (32 channels) of row r1 of every step of
+            // 32 chunks.  Lanes of the upper channel half take their words in the order
+            // 2 3 0 1, so that the eight lanes of a store phase meet all banks.
+            constexpr int kPerRow = D / 32, kStepRows = 32 / kPerRow;
+            const int r1 = lane / kPerRow, c = lane % kPerRow;
+            const bool swap = c >= 2;
+            const uint32_t x0 = (uint32_t)((((c & 1) * 4) ^ (swap ? 2 : 0) ^ (r1 & 7)) << 4);
+            uint32_t j = 0, tiles = 0;
+            bool ok = true;
+            for (Walk w = start(); w.next(a, p);) {
+                const int T = p.t1 - p.t0;
                 const int nblk = (p.L + a.bs - 1) >> bs_shift;
                 const int32_t *pages = a.page_table + (size_t)p.row * a.max_pages;
                 // Page ids 32 blocks at a time, one a lane, the next window in flight.
                 const int blk0 = p.t0 * bpt, blk1 = min(nblk, p.t1 * bpt);
-                auto load_win = [&](int first) -> int {
-                    const int blk = blk0 + first + lane;
+                auto load_win = [&](int w32) -> int {
+                    const int blk = blk0 + w32 * 32 + lane;
                     return blk < blk1 ? pages[blk] : -1;
                 };
-                int win_cur = load_win(0), win_next = load_win(32);
-                for (int t = 0; t < p.t1 - p.t0; ++t, ++tiles) {
-                    const uint32_t st = tiles % kRaw;
+                int win_cur = load_win(0), win_next = load_win(1), win = 0;
+                auto issue = [&](int t) -> uint32_t {  // tile t of the piece; its valid blocks
+                    const uint32_t at = tiles + (uint32_t)t, st = at % kRaw;
+                    if (at >= kRaw) ok = ok && mbar_wait_bounded(&raw_free[st], ((at / kRaw) - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return 0u;
                     const int first = t * bpt;
-                    if (first > 0 && first % 32 == 0) {
+                    if (first >> 5 != win) {
                         win_cur = win_next;
-                        win_next = load_win(first + 32);
+                        ++win;
+                        win_next = load_win(win + 1);
                     }
                     int page = __shfl_sync(0xffffffffu, win_cur, (first + lane) & 31);
                     const bool there = lane < bpt && blk0 + first + lane < blk1;
@@ -727,16 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!there) page = -1;
                     const uint32_t mask = __ballot_sync(0xffffffffu, page >= 0);
-                    if (tiles >= kRaw) ok = mbar_wait_bounded(&raw_free[st], ((tiles / kRaw) - 1) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
                     constexpr int kRunCodes = 16 * D / 2, kRunScales = 16 * D / 16;
                     const uint32_t base = raw_s + st * SM::kRawStage + lane * 16;
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16 / kLoadWarps; ++k) {
-                        const int run = lw + kLoadWarps * k;
+                    for (int k = 0; k < 3; ++k) {
+                        const int run = warp - 1 + 3 * k;
                         const int pg = __shfl_sync(0xffffffffu, page, (run << 4) >> bs_shift);
-                        if (pg >= 0) {
+                        if (run < kKeys / 16 && pg >= 0) {
                             const size_t at16 = ((((size_t)pg * a.hkv + p.h) << bs_shift) >> 4) +
                                                 (run & ((a.bs >> 4) - 1));  // run of 16 keys in the cache
                             const uint8_t *gk = a.c.k + at16 * kRunCodes + lane * 16;
@@ -758,14 +712,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&raw_full[st]))
                                  : "memory");
-                    if (lw == 0 && lane == 0) {
-                        raw_mask[st] = mask;
-                        mbar_arrive(&raw_full[st]);
+                    return mask;
+                };
+                uint32_t masks[3];  // of this tile and the next two
+                masks[0] = issue(0);
+                masks[1] = T > 1 ? issue(1) : 0u;
+                for (int t = 0; t < T; ++t) {
+                    masks[2] = t + 2 < T ? issue(t + 2) : 0u;
+                    const uint32_t at = tiles + (uint32_t)t, st = at % kRaw;
+                    ok = ok && mbar_wait_bounded(&raw_full[st], (at / kRaw) & 1);
+                    const uint32_t mask = masks[0];
+                    masks[0] = masks[1];
+                    masks[1] = masks[2];
+                    const int left = p.L - (p.t0 + t) * kKeys;  // rows of the tile below the length
+                    const bool whole_tile = left >= kKeys && mask == (1u << bpt) - 1u;
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++j) {
+                        if (j >= kSlots)
+                            ok = ok && mbar_wait_bounded(&slot_free[j % kSlots], ((j / kSlots) - 1) & 1);
+                        if (kv == 0 && tid == 32) {
+                            uint32_t m16 = 0;
+                            for (int x = 0; x < kKeys / 16; ++x)
+                                m16 |= ((mask >> ((x * 16) >> bs_shift)) & 1u) << x;
+                            tile_mask[at & 3] = m16;
+                        }
+                        const uint32_t code_at = raw_s + st * SM::kRawStage + kv * SM::kCodes + lane * 16;
+                        const uint32_t scale_at = raw_s + st * SM::kRawStage + 2 * SM::kCodes + kv * SM::kScales +
+                                                  lane * 2;
+                        const uint32_t dst = slots_s + (j % kSlots) * SM::kTile + (c / 2) * SM::kHalf + r1 * 128 + x0;
+                        constexpr int kSteps = (kKeys / kStepRows + 2) / 3;
+                        uint32_t xs[kSteps][4];
+                        uint16_t sf[kSteps];
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const int step = warp - 1 + 3 * k;
+                            if (step < kKeys / kStepRows) {
+                                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(xs[k][0]), "=r"(xs[k][1]), "=r"(xs[k][2]), "=r"(xs[k][3])
+                                             : "r"(code_at + step * 512));
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(sf[k]) : "r"(scale_at + step * 64));
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const int step = warp - 1 + 3 * k;
+                            if (step >= kKeys / kStepRows) break;
+                            if (!whole_tile) {
+                                const int r = step * kStepRows + r1;
+                                if (r >= left || !((mask >> (r >> bs_shift)) & 1u)) sf[k] = 0;  // counts as 0
+                            }
+                            const uint32_t s2 = e4m3x2_to_f16(sf[k]);
+                            const uint32_t sw[2] = {__byte_perm(s2, s2, swap ? 0x3232 : 0x1010),
+                                                    __byte_perm(s2, s2, swap ? 0x1010 : 0x3232)};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t y[4];
+                                e2m1x8_to_f16(swap ? xs[k][i ^ 2] : xs[k][i], y);
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) y[z] = mul_f16x2(y[z], sw[i / 2]);
+                                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                                 (dst + step * (kStepRows * 128)) ^ (i << 4)),
+                                             "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                                             : "memory");
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        mbar_arrive(&slot_full[j % kSlots]);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&raw_free[st]);
                 }
+                tiles += (uint32_t)T;
             }
             cp_async_wait<0>();
-            if (!ok && lw < kLoadWarps && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+            if (!ok && lane == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
         }
         __syncwarp();
         set_regs<kLaunchRegs, true>();
@@ -774,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
 
     // The errors of every sequence.
     for (int u = cta * kThreads + tid; u < units; u += gridDim.x * kThreads) chunk_unit(a, u, a.err);
@@ -792,10 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __threadfence();
     for (Walk w = start(); w.next(a, p);) {
         if (p.t0 == 0 && p.t1 == p.cnt) continue;
-        const int W = sh_w, G = sh_ctas;
-        const int q0 = (int)((((long long)p.ustart + 1) * G - 1) / W);
-        const int q1 = (int)((((long long)p.ustart + p.cnt) * G - 1) / W);
-        const int odd = entry_of(q0, W, G) < p.ustart ? 1 : 0;  // only q0's share can begin before the unit
+        // CTAs q0 .. q1 whose shares meet the unit; only q0's can begin before it
+        const int W = sh_w, G = sh_ctas, own = sh_own.x;
+        const int q0 = own > 0 ? sh_own.y : (int)((((long long)p.ustart + 1) * G - 1) / W);
+        const int q1 = own > 0 ? q0 + own - 1 : (int)((((long long)p.ustart + p.cnt) * G - 1) / W);
+        const int odd = own == 0 && entry_of(q0, W, G) < p.ustart ? 1 : 0;
         // a warp 32 rows and four channels of them at a time, a lane a row
         const int k = q1 - q0 + 1, items = (p.rows + 31) / 32 * (D / 4);
         const int i0 = items * (cta - q0) / k, i1 = items * (cta - q0 + 1) / k;
