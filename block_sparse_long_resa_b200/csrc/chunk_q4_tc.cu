@@ -44,7 +44,7 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers of the launch");
 constexpr int kPieceTiles = 8;          // tiles a CTA takes in the time that a second piece adds
 constexpr int kMinTiles = 2;            // tiles a CTA takes at least, when there are few
-constexpr int kChain = 4;               // tiles whose P V add up in tensor memory
+constexpr int kChain = 2;               // tiles whose P V add up in tensor memory
 constexpr float kShift = 12.f;          // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 3.f;           // growth of the maximum tolerated before rescaling
 
@@ -471,25 +471,24 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
                 const float nb = mx == -INFINITY ? 0.f : kShift - mx;
                 const uint64_t rs2 = pack2(rs, rs), nb2 = pack2(nb, nb), minus = pack2(-1.f, -1.f);
                 uint64_t ls[2] = {0ull, 0ull};
-                uint32_t sv[2][16];
-                tc::tmem_ld16(scol, sv[0]);
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t col = scol + 64 * hf + 16 * c;
-                        uint32_t (&x)[16] = sv[c & 1];
+                    for (int c = 0; c < 2; ++c) {
+                        const int k0 = 64 * hf + 32 * c;
+                        uint32_t x[32];
+                        tc::tmem_ld32(scol + k0, x);
                         tc::tmem_wait_ld();
-                        if (c < 3 || hf == 0) tc::tmem_ld16(col + 16, sv[(c + 1) & 1]);
                         if (!full) {
-                            const int left = ((tm >> (4 * hf + c)) & 1u) ? lim - t0 - 64 * hf - 16 * c : 0;
+                            const int left0 = ((tm >> (k0 / 16)) & 1u) ? lim - t0 - k0 : 0;
+                            const int left1 = ((tm >> (k0 / 16 + 1)) & 1u) ? lim - t0 - k0 : 0;
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (k >= left) x[k] = 0xff800000u;
+                            for (int k = 0; k < 32; ++k)
+                                if (k >= (k < 16 ? left0 : left1)) x[k] = 0xff800000u;
                         }
-                        uint32_t pw[16];  // 8 columns of hi, 8 of lo
+                        uint32_t pw[32];  // of 16 keys 8 columns of hi, 8 of lo
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < 16; ++k) {
                             float p0, p1, l0, l1;
                             unpack2(fma2(pack2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), rs2, nb2),
                                     p0, p1);
@@ -501,10 +500,10 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
                             const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
                             const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
                             unpack2(fma2(pack2(h0, h1), minus, pp), l0, l1);
-                            pw[k] = pack_f16(h0, h1);
-                            pw[8 + k] = pack_f16(l0, l1);
+                            pw[k / 8 * 16 + k % 8] = pack_f16(h0, h1);
+                            pw[k / 8 * 16 + 8 + k % 8] = pack_f16(l0, l1);
                         }
-                        tc::tmem_st16(col, pw);
+                        tc::tmem_st32(scol + k0, pw);
                     }
                     tc::tmem_wait_st();
                     tc::fence_before_sync();
