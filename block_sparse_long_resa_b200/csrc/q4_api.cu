@@ -6,6 +6,8 @@
 namespace resa {
 namespace {
 
+constexpr int kMaxGridBatch = 65535;  // sequences along a grid's y
+
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The checks of check_cache on a 4-bit cache.
@@ -46,6 +48,7 @@ resa_status_t check_append(const Shape &s, const resa_rope_t *rope, const resa_t
     if (rope->rot_dim > 0 && !rope->inv_freq) return RESA_ERR_NULL;
     if (!isfinite(rope->mscale)) return RESA_ERR_RANGE;
     if (t->f < 1) return RESA_ERR_RANGE;
+    if (s.batch > kMaxGridBatch) return RESA_ERR_UNSUPPORTED;
     const long long q_row = (long long)s.hq * s.d, kv_row = (long long)s.hkv * s.d;
     a->q_stride = t->q_stride ? t->q_stride : q_row;
     a->k_stride = t->k_stride ? t->k_stride : kv_row;
@@ -126,6 +129,7 @@ resa_status_t resa_expand_q4(const resa_config_t *cfg, const resa_cache_q4_t *ca
     RESA_TRY(check_config(cfg, &s));
     RESA_TRY(check_cache_q4(cache, &s, false, &c));
     if (!k_out || !v_out) return RESA_ERR_NULL;
+    if (s.batch > kMaxGridBatch) return RESA_ERR_UNSUPPORTED;
     if (!aligned16(k_out) || !aligned16(v_out)) return RESA_ERR_UNSUPPORTED;
     const WsLayout w = layout_of(s, 0);
     RESA_TRY(check_ws(ws, ws_bytes, w));

@@ -125,21 +125,33 @@ def _ptr(t) -> Optional[int]:
 
 
 @functools.lru_cache(maxsize=None)
-def _current_raw_stream():
-    """A function giving the current device's current stream as a handle: the Stream object
-    that torch.cuda.current_stream() makes costs 3 us a call."""
+def _cuda():
+    """(handle of a device's current stream, current device): the Stream object that
+    torch.cuda.current_stream() makes costs 3 us a call."""
     import torch
     torch.cuda.init()
-    handle, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    return lambda: handle(device())
+    return torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _current_raw_stream()()
+        handle, device = _cuda()
+        return handle(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _stream_at(stream, ws, where: str) -> Optional[int]:
+    """_stream, of a call whose workspace has to be on the current device."""
+    if stream is not None:
+        return _stream(stream)
+    if ws.device.type != "cuda":
+        raise ResaError(4, f"{where}: the workspace is on {ws.device}")
+    handle, device = _cuda()
+    if ws.device.index != device():
+        raise ResaError(4, f"{where}: the workspace is on {ws.device}, not the current device")
+    return handle(ws.device.index)
 
 
 def _check(st: int, where: str):
@@ -177,11 +189,33 @@ def _keep(struct, *tensors):
     return struct
 
 
+def _expect(name: str, t, dtype: str, shape=None):
+    """Refuse a tensor whose memory is not what the C ABI takes it for."""
+    if t is None:
+        return
+    if str(t.dtype) not in tuple("torch." + d for d in dtype.split("|")):
+        raise ResaError(4, f"{name}: {t.dtype}, not {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ResaError(2, f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ResaError(4, f"{name} is not contiguous")
+
+
 def make_cache_q4(k, k_sf, v, v_sf, desc, page_table, seq_len, rows=None, k_scale=None,
                   v_scale=None) -> resa_cache_q4_t:
     """4-bit cache struct over torch tensors k/v [pages][Hkv][b][d/2] uint8 codes, k_sf/v_sf
     [pages][Hkv][b][d/16] float8_e4m3fn group scales, desc / page_table / seq_len / rows as in
     make_cache, and the heads' scales k_scale/v_scale [Hkv] fp32 (None: 1)."""
+    pages, hkv, b, half = k.shape
+    for name, t, dtype, shape in (
+            ("k", k, "uint8", None), ("v", v, "uint8", k.shape),
+            ("k_sf", k_sf, "float8_e4m3fn|uint8", (pages, hkv, b, half // 8)),
+            ("v_sf", v_sf, "float8_e4m3fn|uint8", (pages, hkv, b, half // 8)),
+            ("desc", desc, "bfloat16", (pages, hkv, 2, 2 * half)),
+            ("page_table", page_table, "int32", None),
+            ("seq_len", seq_len, "int32", page_table.shape[:1]), ("rows", rows, "int32", None),
+            ("k_scale", k_scale, "float32", (hkv,)), ("v_scale", v_scale, "float32", (hkv,))):
+        _expect("make_cache_q4: " + name, t, dtype, shape)
     nrows = int(page_table.shape[0])
     return _keep(resa_cache_q4_t(_ptr(k), _ptr(v), _ptr(k_sf), _ptr(v_sf), _ptr(desc),
                                  _ptr(page_table), _ptr(seq_len),
@@ -195,6 +229,8 @@ def make_rope(rot_dim: int, inv_freq, interleaved: bool = False,
               mscale: float = 1.0) -> resa_rope_t:
     """Rotary embedding of the first ``rot_dim`` channels; inv_freq: fp32 device tensor
     [rot_dim / 2] (None when rot_dim is 0)."""
+    if rot_dim:
+        _expect("make_rope: inv_freq", inv_freq, "float32", (rot_dim // 2,))
     return _keep(resa_rope_t(rot_dim, 1 if interleaved else 0,
                              _ptr(inv_freq) if rot_dim else None, mscale), inv_freq)
 
@@ -214,6 +250,12 @@ def _token_stride(t, name: str) -> int:
 def make_tokens(q, k, v, n_new=None, positions=None) -> resa_tokens_t:
     """Fresh tokens of a call: q [batch][f][Hq][d] (or None), k, v [batch][f][Hkv][d] bf16, e.g.
     views of one fused projection output; n_new [batch] and positions [batch][f] int32 or None."""
+    b, f = k.shape[:2]
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t is not None and (str(t.dtype) != "torch.bfloat16" or tuple(t.shape[:2]) != (b, f)):
+            raise ResaError(2, f"make_tokens: {name} is not [batch][f][heads][d] bf16 as k is")
+    _expect("make_tokens: n_new", n_new, "int32", (b,))
+    _expect("make_tokens: positions", positions, "int32", (b, f))
     return _keep(resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),
                                0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"),
                                _token_stride(v, "v"), int(k.shape[1]), _ptr(n_new),
@@ -311,7 +353,7 @@ def resa_append_rope(cfg, cache, rope, tokens, q_out, ws, stream=None):
     """Append fresh tokens to the bf16 cache, queries and keys rotated on the way."""
     _check(lib().resa_append_rope(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
                                   ctypes.byref(tokens), _ptr(q_out), _ptr(ws), ws.numel(),
-                                  _stream(stream)),
+                                  _stream_at(stream, ws, "resa_append_rope")),
            "resa_append_rope")
 
 
@@ -319,14 +361,14 @@ def resa_append_rope_q4(cfg, cache, rope, tokens, q_out, ws, stream=None):
     """resa_append_rope into a 4-bit cache (make_cache_q4)."""
     _check(lib().resa_append_rope_q4(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
                                      ctypes.byref(tokens), _ptr(q_out), _ptr(ws), ws.numel(),
-                                     _stream(stream)),
+                                     _stream_at(stream, ws, "resa_append_rope_q4")),
            "resa_append_rope_q4")
 
 
 def resa_expand_q4(cfg, cache, k_out, v_out, ws, stream=None):
     """Write a 4-bit cache's valid positions into bf16 pages k_out / v_out."""
     _check(lib().resa_expand_q4(ctypes.byref(cfg), ctypes.byref(cache), _ptr(k_out), _ptr(v_out),
-                                _ptr(ws), ws.numel(), _stream(stream)),
+                                _ptr(ws), ws.numel(), _stream_at(stream, ws, "resa_expand_q4")),
            "resa_expand_q4")
 
 
@@ -335,7 +377,8 @@ def resa_sparse_decode_q4(cfg, cache, q, block_idx, block_cnt, max_topk: int, ou
     """resa_sparse_decode over a 4-bit cache."""
     _check(lib().resa_sparse_decode_q4(ctypes.byref(cfg), ctypes.byref(cache), _ptr(q),
                                        _ptr(block_idx), _ptr(block_cnt), max_topk, _ptr(out),
-                                       _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+                                       _ptr(lse), _ptr(ws), ws.numel(),
+                                       _stream_at(stream, ws, "resa_sparse_decode_q4")),
            "resa_sparse_decode_q4")
 
 
@@ -343,7 +386,7 @@ def resa_attention_q4(cfg, cache, f: int, n_new, q, out, lse, ws, stream=None):
     """Causal attention of each sequence's last n_new (None: f) tokens over its 4-bit cache."""
     _check(lib().resa_attention_q4(ctypes.byref(cfg), ctypes.byref(cache), f, _ptr(n_new),
                                    _ptr(q), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                   _stream(stream)),
+                                   _stream_at(stream, ws, "resa_attention_q4")),
            "resa_attention_q4")
 
 

@@ -343,7 +343,9 @@ RESA_API resa_status_t resa_sparse_decode_noalloc(const resa_config_t *cfg,
  * Rows of padding are not read and stay as they were in q_out.  A sequence with
  * n_new = 0 is skipped whatever its length; n_new outside 0 .. f or above
  * seq_len sets RESA_DEVERR_CHUNK and the sequence is skipped.  A block whose
- * page is out of range sets RESA_DEVERR_PAGE and is skipped.  One launch. */
+ * page is out of range sets RESA_DEVERR_PAGE and is skipped.  The sequences'
+ * blocks that hold fresh tokens must be distinct pages.  At most 65535 sequences
+ * a call (more: RESA_ERR_UNSUPPORTED).  One launch. */
 RESA_API resa_status_t resa_append_rope(const resa_config_t *cfg, const resa_cache_t *cache,
                                         const resa_rope_t *rope, const resa_tokens_t *tokens,
                                         void *q_out, void *ws, size_t ws_bytes,
@@ -361,14 +363,15 @@ RESA_API resa_status_t resa_append_rope_q4(const resa_config_t *cfg, const resa_
  * bf16 (the k, v of a resa_cache_t with the same page table, lengths and
  * descriptors).  Positions 0 .. seq_len-1 of the call's sequences are written
  * (values c * s * g rounded once to bf16), all others stay as they were.  A
- * sequence of length 0 is skipped.  One launch. */
+ * sequence of length 0 is skipped.  At most 65535 sequences a call.  One launch. */
 RESA_API resa_status_t resa_expand_q4(const resa_config_t *cfg, const resa_cache_q4_t *cache,
                                       void *k_out, void *v_out, void *ws, size_t ws_bytes,
                                       cudaStream_t stream);
 
 /* Group block-sparse attention over a 4-bit cache: resa_sparse_decode with the
  * same arguments and the same treatment of block lists.  A (sequence, kv head)
- * with block_cnt 0 gives out = 0 and lse = -inf.  One launch. */
+ * with block_cnt 0 gives out = 0 and lse = -inf.  batch * Hkv * (max_topk + 1)
+ * above 2^31 - 1 returns RESA_ERR_RANGE.  One launch. */
 RESA_API resa_status_t resa_sparse_decode_q4(const resa_config_t *cfg,
                                              const resa_cache_q4_t *cache, const void *q,
                                              const int32_t *block_idx, const int32_t *block_cnt,
@@ -384,8 +387,8 @@ RESA_API resa_status_t resa_sparse_decode_q4(const resa_config_t *cfg,
  * log.  Rows r >= n are padding: not read, and left as they were in out and lse.
  * A sequence with n = 0 is skipped whatever its length; n outside 0 .. f or
  * above L sets RESA_DEVERR_CHUNK and the sequence is skipped.
- * f must be 1 or in 1 .. max_chunk of the workspace, and f * g at most 16384
- * (more: RESA_ERR_UNSUPPORTED).  One launch. */
+ * f * g <= 16 needs no max_chunk; else f must be in 1 .. max_chunk of the
+ * workspace, and f * g at most 16384 (more: RESA_ERR_UNSUPPORTED).  One launch. */
 RESA_API resa_status_t resa_attention_q4(const resa_config_t *cfg, const resa_cache_q4_t *cache,
                                          int32_t f, const int32_t *n_new_opt, const void *q,
                                          float *out, float *lse_opt, void *ws, size_t ws_bytes,

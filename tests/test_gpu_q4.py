@@ -522,3 +522,191 @@ def test_graph_capture_and_replay(cuda_device):
         second()
         assert torch.equal(got, out) and torch.equal(got1, out1) and torch.equal(gq, q_out)
     assert p.status() == 0
+
+
+# ------------------------------------------------------------- further shapes, splits and streams
+
+@pytest.mark.parametrize("inter", [False, True], ids=["half", "adjacent"])
+@pytest.mark.parametrize("rot", [16, 48, 112])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_partial_rotations(cuda_device, d, rot, inter):
+    """Rotations of a part of the head, positions of any sign."""
+    if rot > d:
+        rot = 32
+    p = Problem(11, [37, 50], 4, 2, d, 16, cuda_device)
+    t = Tokens(p, 37, [37, 20], False)
+    pos = np.stack([np.arange(37) * 1001 - 17000, np.arange(37) - 18]).astype(np.int32)
+    inv = (1e4 ** (-np.arange(0, rot, 2) / rot)).astype(np.float32)
+    t_pos, t_inv = torch.from_numpy(pos).to(cuda_device), torch.from_numpy(inv).to(cuda_device)
+    tok = R.make_tokens(t.tq, t.tk, t.tv, n_new=t.n, positions=t_pos)
+    k, v = (torch.from_numpy(x).to(cuda_device).bfloat16() for x in (p.k16, p.v16))
+    q_out = torch.zeros_like(t.tq)
+    R.resa_append_rope(p.cfg, R.make_cache(k, v, p.desc, p.t_table, p.t_len),
+                       R.make_rope(rot, t_inv, interleaved=inter), tok, q_out, p.ws)
+    assert p.status() == 0
+    for i, (L, n) in enumerate(((37, 37), (50, 20))):
+        at = np.arange(L - n, L)
+        page, slot = p.table[i, at // 16], at % 16
+        want = q4.bf16(q4.rotate(t.k[i, :n], pos[i, :n], inv, rot, inter))
+        np.testing.assert_array_equal(f64(k)[page, :, slot], want)
+        q = q4.rotate(t.q[i, :n], pos[i, :n], inv, rot, inter)
+        tol = np.abs(q) * 2.0 ** -8 + 2.0 ** -20 * 2 * np.abs(t.q[i, :n]).max()
+        assert (np.abs(f64(q_out)[i, :n] - q) <= tol).all()
+
+
+def test_expand_to_pages_aligned_to_16_bytes(cuda_device):
+    p = Problem(21, [100, 3], 4, 2, 64, 16, cuda_device)
+    n = p.num_pages * 2 * 16 * 64
+    want_k, want_v = (torch.zeros(n, dtype=torch.bfloat16, device=cuda_device) for _ in range(2))
+    raw = torch.zeros(2, n + 64, dtype=torch.bfloat16, device=cuda_device)
+    k, v = raw[0, 8:8 + n], raw[1, 8:8 + n]
+    assert k.data_ptr() % 32 == 16
+    R.resa_expand_q4(p.cfg, p.cache4(), want_k, want_v, p.ws)
+    R.resa_expand_q4(p.cfg, p.cache4(), k, v, p.ws)
+    assert torch.equal(k, want_k) and torch.equal(v, want_v) and p.status() == 0
+    assert (raw[:, :8] == 0).all() and (raw[:, 8 + n:] == 0).all()
+
+
+SPLITS = [  # layout, lens, width of the table in keys: whole units, even shares, the line of blocks
+    ((28, 4, 128, 16), [5, 700, 1900], 2048),
+    ((28, 4, 128, 16), [5, 700, 1900], 40000),
+    ((32, 2, 64, 32), [1, 64, 3000, 9], 40000),
+    ((16, 8, 128, 16), [1 + 7 * i for i in range(40)], 40000),       # more units than SMs
+    ((8, 8, 64, 64), [3000] + [2 + i for i in range(17)], 40000),    # one long unit among short ones
+    ((14, 2, 128, 16), [20000, 1, 19999], 20100),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SPLITS)))
+def test_attention_splits(cuda_device, case):
+    """The same rows whichever way the units are shared out among the CTAs."""
+    (hq, hkv, d, b), lens, width = SPLITS[case]
+    extra = max(0, width // b - (-(-max(lens) // b)))
+    p = Problem(61 + case, lens, hq, hkv, d, b, cuda_device, extra_pages=extra)
+    q = q4.bf16(p.rng.standard_normal((len(lens), hq, d)))
+    tq = torch.from_numpy(q).to(cuda_device).bfloat16()
+    out, lse = chunk(p, 1, None, tq.unsqueeze(1).contiguous())
+    assert p.status() == 0
+    for i in sorted({0, 1, len(lens) // 2, len(lens) - 1}):
+        for h in range(hkv):
+            r = slice(h * p.g, (h + 1) * p.g)
+            check_rows(p, out[i, 0, r], lse[i, 0, r], q[i, r], i, h, None, np.full(p.g, lens[i]))
+    o2, l2 = chunk(p, 1, None, tq.unsqueeze(1).contiguous())
+    assert np.array_equal(out, o2) and np.array_equal(lse, l2)
+
+
+@pytest.mark.parametrize("layout,lens,f", [((28, 4, 128, 16), [3000, 130, 900], 40),
+                                           ((16, 8, 64, 32), [70 + 40 * i for i in range(24)], 20)],
+                         ids=["few", "many"])
+def test_chunk_large_logits_and_splits(cuda_device, layout, lens, f):
+    """The running maximum grows in the middle of a sequence; units shared among CTAs or many a CTA."""
+    hq, hkv, d, b = layout
+    p = Problem(72, lens, hq, hkv, d, b, cuda_device, max_chunk=f, key_size=4.0, extra_pages=60)
+    q = q4.bf16(p.rng.standard_normal((len(lens), f, hq, d)) * 6)
+    out, lse = chunk(p, f, None, torch.from_numpy(q).to(cuda_device).bfloat16())
+    assert p.status() == 0
+    for i in sorted({0, 1, len(lens) - 1}):
+        limit = np.repeat(np.arange(lens[i] - f, lens[i]) + 1, p.g)
+        for h in range(0, hkv, 3):
+            r = slice(h * p.g, (h + 1) * p.g)
+            check_rows(p, out[i, :, r].reshape(-1, d), lse[i, :, r].reshape(-1),
+                       q[i, :, r].reshape(-1, d), i, h, None, limit)
+
+
+def test_queries_of_every_size(cuda_device):
+    """Rows of zeros, of bf16's smallest and of large values, in one call each way."""
+    p = Problem(73, [600], 8, 1, 128, 16, cuda_device, max_chunk=16)
+    size = np.array([0.0, 1e-38, 1e-30, 1e-10, 1.0, 30.0, 100.0, 1e-3])
+    for f in (1, 16):
+        q = q4.bf16(p.rng.standard_normal((1, f, 8, 128)) * size[:, None])
+        out, lse = chunk(p, f, None, torch.from_numpy(q).to(cuda_device).bfloat16())
+        assert p.status() == 0
+        limit = np.repeat(np.arange(600 - f, 600) + 1, 8)
+        check_rows(p, out[0].reshape(-1, 128), lse[0].reshape(-1), q[0].reshape(-1, 128), 0, 0, None, limit)
+
+
+def test_non_finite_values_stay_in_their_rows(cuda_device):
+    """A NaN query row gives NaN, a NaN group scale the rows that see it; the others are untouched."""
+    p = Problem(74, [200, 300], 8, 2, 64, 16, cuda_device, max_chunk=10)
+    for f in (1, 10):
+        q = torch.randn(2, f, 8, 64, device=cuda_device).bfloat16()
+        good, _ = chunk(p, f, None, q)
+        bad = q.clone()
+        bad[0, 0, 1, 3] = float("nan")
+        out, lse = chunk(p, f, None, bad)
+        assert np.isnan(out[0, 0, 1]).all() and np.isnan(lse[0, 0, 1])
+        out[0, 0, 1] = good[0, 0, 1]
+        assert np.array_equal(out, good)
+    sf = p.k_sf.view(torch.uint8)
+    page = int(p.table[1, 5])
+    keep = sf[page, 0, 3, 0].item()
+    sf[page, 0, 3, 0] = 0x7f
+    out, _ = chunk(p, 1, None, q[:, :1].contiguous())
+    sf[page, 0, 3, 0] = keep
+    ref, _ = chunk(p, 1, None, q[:, :1].contiguous())
+    assert np.isnan(out[1, 0, :4]).all()
+    out[1, 0, :4] = ref[1, 0, :4]
+    assert np.array_equal(out, ref) and p.status() == 0
+
+
+def test_two_streams_with_a_workspace_each(cuda_device):
+    """Calls on two streams at once, each with its own workspace and outputs."""
+    dev = cuda_device
+    ps = [Problem(75 + i, [3000, 500], 28, 4, 128, 16, dev, max_chunk=12, extra_pages=2000) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    data = []
+    for p in ps:
+        q = torch.randn(2, 12, 28, 128, device=dev).bfloat16()
+        data.append((q, torch.zeros(2, 12, 28, 128, device=dev), torch.zeros(2, 28, 128, device=dev)))
+    want = []
+    for p, (q, out, o1) in zip(ps, data):
+        R.resa_attention_q4(p.cfg, p.cache4(), 12, None, q, out, None, p.ws)
+        R.resa_attention_q4(p.cfg, p.cache4(), 1, None, q[:, 0].contiguous(), o1, None, p.ws)
+        want.append((out.clone(), o1.clone()))
+    torch.cuda.synchronize()
+    firsts = [q[:, 0].contiguous() for q, _, _ in data]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, s, (q, out, o1), q1 in zip(ps, streams, data, firsts):
+            R.resa_attention_q4(p.cfg, p.cache4(), 12, None, q, out, None, p.ws, stream=s)
+            R.resa_attention_q4(p.cfg, p.cache4(), 1, None, q1, o1, None, p.ws, stream=s)
+    torch.cuda.synchronize()
+    for p, (_, out, o1), (a, b) in zip(ps, data, want):
+        assert torch.equal(out, a) and torch.equal(o1, b) and p.status() == 0
+
+
+def test_layer_cache_q4_from_nothing(cuda_device):
+    """The holder: an empty cache, tokens appended in two calls, selection and attention on it."""
+    from block_sparse_long_resa_b200.cache import LayerCacheQ4, workspace
+    dev = cuda_device
+    table = torch.arange(12, dtype=torch.int32, device=dev).view(2, 6).flip(1).contiguous()
+    lc = LayerCacheQ4.empty(12, 2, 16, 64, table, k_scale=torch.full((2,), 0.5, device=dev))
+    cfg = R.make_config(4, 2, 64, 16)
+    ws = workspace(cfg, lc.batch, lc.max_pages, 0, dev)
+    rng = np.random.default_rng(76)
+    k = q4.bf16(rng.standard_normal((2, 50, 2, 64)))
+    v = q4.bf16(rng.standard_normal((2, 50, 2, 64)))
+    up = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(dev).bfloat16()
+    for a, e in ((0, 41), (41, 50)):
+        tk, tv = up(k[:, a:e]), up(v[:, a:e])
+        lc.seq_len.fill_(e)
+        R.resa_append_rope_q4(cfg, lc.struct(), R.make_rope(0, None), R.make_tokens(None, tk, tv), None, ws)
+    q = up(rng.standard_normal((2, 4, 64)))
+    topk = torch.full((2,), 9, dtype=torch.int32, device=dev)     # every block
+    idx = torch.zeros(2, 2, 10, dtype=torch.int32, device=dev)
+    cnt = torch.zeros(2, 2, dtype=torch.int32, device=dev)
+    R.resa_select_blocks(cfg, lc.select_struct(), q, topk, 9, idx, cnt, None, ws)
+    assert cnt.tolist() == [[4, 4]] * 2
+    a, b = torch.zeros(2, 4, 64, device=dev), torch.zeros(2, 4, 64, device=dev)
+    R.resa_sparse_decode_q4(cfg, lc.struct(), q, idx, cnt, 9, a, None, ws)
+    R.resa_attention_q4(cfg, lc.struct(), 1, None, q, b, None, ws)
+    assert torch.equal(a, b)                                       # the same blocks in the same order
+    assert R.resa_check_device_status(ws, raise_on_error=False) == 0
+    for i in range(2):
+        for h in range(2):
+            kc, ks = q4.quantise(k[i, :, h], np.full((50, 1), 0.5, np.float32))
+            vc, vs = q4.quantise(v[i, :, h], np.ones((50, 1), np.float32))
+            o, _, w, mag, vsum = q4.attention(f64(q)[i, 2 * h:2 * h + 2], q4.values(kc, ks) * 0.5,
+                                              q4.values(vc, vs), [50, 50], 0.125)
+            tol, _ = attention_tolerance(mag[:, None], 50, w, vsum)
+            assert (np.abs(f64(a)[i, 2 * h:2 * h + 2] - o) <= tol).all()
