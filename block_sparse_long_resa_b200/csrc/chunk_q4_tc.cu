@@ -4,29 +4,42 @@
 //
 // Rows of one (sequence, kv head) are rho = r * g + j (chunk row r, group head j),
 // taken 256 at a time (a row group: two M = 128 tiles, m = 0 and 1).  A unit is
-// (sequence, kv head, row group) with its tiles of 128 keys.  The tiles of all
-// units form one line of W entries; CTA c of G takes [cW/G, (c+1)W/G), a run of
-// pieces, each one unit's.  A unit inside one CTA is written directly; of a
-// unit that spans several, each stores its partial (o, max, sum), and after a
-// bounded grid barrier (cooperative launch, one CTA per SM) those CTAs merge an
-// equal share of its rows, in CTA order.
+// (sequence, kv head, row group) with its tiles of 128 keys.  Every unit is cut
+// into even shares, one a CTA, or, where that would give some CTAs much more than
+// others, the tiles of all units form one line of W entries and CTA c of G takes
+// [cW/G, (c+1)W/G), a run of pieces, each one unit's.  A unit inside one CTA is
+// written directly; of a unit that spans several, each stores its partial (o, max,
+// sum), and after a bounded grid barrier (cooperative launch, one CTA per SM)
+// those CTAs merge an equal share of its rows, in CTA order.
 //
 // Warp roles (384 threads; registers moved from warpgroup 0 to the others):
-//   warp 0      TMEM owner and MMA issuer (one thread);
+//   warp 0      TMEM owner and MMA issuer;
 //   warps 1-3   bring the 4-bit tiles in (cp.async, three raw stages) and expand
 //               them, c * s in fp16 (exact), into 128-byte swizzled operand tiles:
 //               a ring of three 32 KB slots K0 V0 K1 V1 ..;
 //   warps 4-7, 8-11   softmax of M tile 0 and 1, one thread a row.
 // Per M tile the chain is QK^T(i) -> softmax -> P V(i) -> QK^T(i+1); the two M
-// tiles run half a period apart, so one's MMAs fill the other's softmax.
+// tiles run half a period apart, so one's MMAs fill the other's softmax, and P V
+// of a tile's first 64 keys runs while the softmax makes the others' weights.
 //
 // Precision.  q enters as fp16 scaled per row by a power of two (its 8 bits stay
-// exact), so Q K^T has exact products.  P enters as fp16 hi + lo (22 bits), both
-// over the tile's S in tensor memory, 32 keys (16 + 16 columns) at a time.  The
-// matrix unit truncates when it adds to its fp32 accumulator, which over a long
-// sequence would be a bias of 10^-5, so P V starts from zero at every tile and
-// the softmax thread adds the tile's O to its row in registers (fused with the
-// rescaling, o = o * 2^(m - m') + tile), where additions round to nearest.
+// exact), so Q K^T has exact products.  P enters as fp16 hi + lo (22 bits; fp16
+// alone would be 1.4e-4 off), both over the tile's S in tensor memory, 16 keys
+// (8 + 8 columns) at a time: P V takes twice the MMAs.  The matrix unit truncates
+// when it adds to its fp32 accumulator: 1.1e-5 off after 1024 additions.  So O
+// starts from zero every kChain tiles and is then added to its row in registers,
+// where additions round to nearest: 7e-7 off for 2 tiles, 1.2e-6 for 4, 2.4e-6
+// for 8, and 2 takes 1.2 % and 1.6 % longer than 4 and 8.
+//
+// Measured (28 q / 4 kv heads, d 128, 32 rows against 4 x 65536 tokens: 120 GFLOP,
+// 1.5 times that in MMAs, 153 MB): 185 us, 0.65 PFLOP/s, 0.97 PFLOP/s in MMAs.
+// Of a tile's 4900 cycles the chain of one M tile takes all: maximum 500, weights
+// 2600 (128 exponentials a thread at 4 a cycle and SM quarter are 1024), P V of the
+// second half 490, Q K^T 780.  An MMA with A in shared memory takes 97 cycles
+// whatever its N up to 128, so 64-key tiles with S double-buffered, which hide
+// the chain, double Q K^T and measured 250 us; two threads a row (O added up in
+// memory, 4.5e-6 off) 212 us; four converter and two loader warps beside the MMA
+// warp, with fewer registers for the rows, 191 us.
 #include "q4_common.cuh"
 #include "tc_common.cuh"
 

@@ -12,8 +12,8 @@
 // max, sum), and behind a grid barrier they add them up, each an equal share of
 // the rows, in CTA order, so the result does not depend on the arrival order.
 //
-// Inside a piece, warp w takes every eighth step of 32 positions (two tiles of
-// 16) through a private cp.async ring of kStages steps and keeps its own
+// Inside a piece, warp w of kWarps takes every kWarps-th step of 32 positions (two
+// tiles of 16) through a private cp.async ring of kStages steps and keeps its own
 // online softmax; the warps' states are merged at the end of the piece.
 //
 // The MMAs are m16n8k16 fp16 with the operands swapped, S^T = K Q^T and
@@ -26,7 +26,15 @@
 //      pairs up the two tokens of a register with byte permutes.
 // c * s is exact in fp16.  q is scaled by a power of two per row into fp16's
 // range (its 8 bits stay exact), and P enters as fp16 hi + lo (22 bits) scaled
-// by 2^kShift, so the products lose nothing that fp32 accumulation keeps.
+// by 2^kShift, so the products lose nothing that fp32 accumulation keeps.  A step's
+// products start from zero and join the row in fp32 registers (see below).
+//
+// Measured (28 q / 4 kv heads, d 128): every position of one 262144-token sequence,
+// 151 MB, 52 us, 2.9 TB/s.  Instructions bound it: a warp's step of 32 tokens is
+// about 800 of them, issued at 2 a cycle and SM in 35 us; the rest is the first loads,
+// the barrier and the merge.  16 warps for 12 and two accumulator chains for one
+// changed nothing.  A list of 10 % of the same sequence's blocks, 15 MB: 16 us, nearly
+// all of it latency (list, page, tile, barrier, partials).
 #include "q4_common.cuh"
 
 namespace resa {
