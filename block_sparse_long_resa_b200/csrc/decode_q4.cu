@@ -4,7 +4,8 @@
 // each 4-bit key and value once.
 //
 // Work.  A unit is a (sequence, kv head) with its list of blocks.  Short units go
-// to a CTA each.  Else every unit is cut into even shares, one a CTA, or, where
+// to a CTA each, longer ones to a thread-block cluster each, whose CTAs take even
+// shares and merge them through its shared memory.  Else every unit is cut into even shares, one a CTA, or, where
 // that would leave some CTAs with much more than others (many unequal units), the
 // blocks of all units form one line of W entries, and CTA c of G takes entries
 // [cW/G, (c+1)W/G), a run of pieces, each one unit's.  A unit inside one CTA is
@@ -35,7 +36,11 @@
 // the barrier and the merge.  16 warps for 12 and two accumulator chains for one
 // changed nothing.  A list of 10 % of the same sequence's blocks, 15 MB: 16 us, nearly
 // all of it latency (list, page, tile, barrier, partials).
+#include <cooperative_groups.h>
+
 #include "q4_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace resa {
 namespace {
@@ -44,14 +49,26 @@ template <int D, int NT>
 struct Q4Warps {
     static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 4 : 4;
 };
-// Units of at most so many keys are not split, by the width of the query tile.  Measured
-// (28 q / 4 kv heads, d 128, batch 1, 8, 32): 1024 keys 11 us whole and 16, 16, 19 us split,
-// 2048 keys 16-17 and 16, 17, 24, 4096 keys 26-27 and 12, 20, 33; with 16 heads a group 512
-// keys 11 and 12-13 us, 1024 keys 15 and 13, 13, 24.
-constexpr int kWholeKeys[2] = {2048, 768};
+// Units of at most so many keys are not split, by the width of the query tile, where a
+// cluster is no choice and where it is.  Measured (28 q / 4 kv heads, d 128, batch 16): 1024
+// keys 11.4 us whole, 11.4 by clusters of 2, 2048 keys 17 and 14 and, over the grid, 16-24;
+// batch 1: 512 keys 8.6 whole and 9.7 by clusters of 8, 1024 keys 11.0 and 10.1; with 16
+// heads a group 512 keys 11.1 and 11.5, 1024 keys 15 and 12.0.
+constexpr int kWholeKeys[2] = {2048, 768}, kWholeNear[2] = {768, 512};
 // With units for most of the SMs: 128 units of 8192 keys 50 us whole and 54 split, 256 units of
 // 1 .. 2500 keys 30 and 57.
 constexpr int kWholeKeysMany = 8192;
+// Clusters, which leave out the grid barrier and the partials' way through L2, but share by
+// the unit where the grid shares by all units' keys: a CTA takes at most kClusterKeys, and at
+// most kClusterMore more than over the grid.  Measured, clusters and grid: batch 1, 4096 keys
+// 11.3 and 12.1 us, 8192 keys 13.7 and 12.4; batch 2, 8192 keys 13.8 and 14.7, 16384 keys 19.3
+// and 17.3; batch 8 (clusters of 4), 4096 keys 14.1 and 16.9; 16 heads a group, batch 1, 2048
+// keys 12.5 and 13.7, 4096 keys 14.5 and 13.8.  Unequal lengths favour the grid (16 sequences
+// of 17 .. 9001 keys, 16 heads a group: 26.7 and 24.6), hence the first bound.
+constexpr int kClusterKeys[2] = {1024, 512}, kClusterMore[2] = {600, 400};
+// Units whose clusters run at once (74, 33 and 15 clusters of 2, 4 and 8 CTAs fit; 16 units by
+// 8, a second wave, 17 us where 14 units take 10).  Clusters of 16 gained 0.1 to 0.7 us.
+constexpr int cluster_units(int cl) { return cl == 8 ? 14 : cl == 4 ? 32 : 72; }
 constexpr int kPieceKeys = 2048;   // keys a CTA takes in the time that a second piece adds
 constexpr float kShift = 13.f;     // P is stored as 2^kShift * exp2(x - m)
 constexpr float kSlack = 2.f;      // growth of the maximum tolerated before rescaling
@@ -148,6 +165,7 @@ struct DecodeQ4Args {
     uint32_t *err;
     RowMap rm;
     int f, max_topk, batch, hq, hkv, g, max_pages, num_pages, bs;
+    int cluster;  // CTAs a unit takes (a thread-block cluster), without a grid barrier
     float scale_log2;
 };
 
@@ -210,8 +228,8 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
 
     if (tid < 2) sh_part[tid].rows = 0;
     if (tid == 0) sh_most = 0;
-    // Whole units (no grid barrier): CTA u takes unit u.  Else prefix sums of the units'
-    // blocks: thread t sums units [t * per, ...).
+    // Without a grid barrier a unit has a CTA or a cluster of them, in even shares.  Else
+    // prefix sums of the units' blocks: thread t sums units [t * per, ...).
     const bool split = a.grid_bar != nullptr;
     const int per = (units + kThreads - 1) / kThreads;
     const bool kept = per == 1 && split;  // the units' data are in sh_units
@@ -300,7 +318,12 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             __syncthreads();
         }
     } else {
-        x1 = unit_of(cta, false).cnt;
+        const int cnt = unit_of(cta / a.cluster, false).cnt, rank = cta % a.cluster;
+        const int share = max(max(1, 32 * kWarps / a.bs), (cnt + a.cluster - 1) / a.cluster);
+        x0 = min(cnt, rank * share);
+        x1 = min(cnt, x0 + share);
+        own = (cnt + share - 1) / share;
+        own_first = cta - rank;
     }
 
     auto orow_of = [&](int b, int h, int rho) -> size_t {
@@ -315,11 +338,18 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     auto lse_of = [&](float ms, float ls) -> float {
         return ls > 0.f ? (ms - kShift + log2f(ls)) * 0.6931471805599453f : ls == 0.f ? -INFINITY : ls;
     };
-    int u = !split ? cta : x0 < x1 ? sh_unit : 0;
+    int u = !split ? cta / a.cluster : x0 < x1 ? sh_unit : 0;
     int ustart = split && x0 < x1 ? sh_first : 0;
     const int sub_shift = a.bs == 64 ? 2 : a.bs == 32 ? 1 : 0;  // tiles a block
     uint8_t *ring = smem + (size_t)warp * kStages * SM::kStage;
     const uint32_t ring_s = smem_u32(ring);
+    // The warps' merge, over the rings.  A row's channels lie there (and in the partials) in
+    // the order of the lanes, channel r * D/8 + 2 t2 + z at place 16 t2 + 2 r + z, and rows
+    // are padded by 4, so that a store's lanes meet all banks.
+    constexpr int kRow = D + 4;
+    float *wm = reinterpret_cast<float *>(smem);
+    float *wl = wm + kWarps * kRows, *wf = wl + kWarps * kRows;
+    float *wo = wf + kWarps * kRows;
 
     for (int x = x0; x < x1; ++u) {
         Unit un;
@@ -679,13 +709,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
                 l[n][k2] += __shfl_xor_sync(0xffffffffu, l[n][k2], 16);
             }
         __syncthreads();  // every ring is drained
-        // Merge the warps.  A row's channels lie in shared memory (and in the partials) in
-        // the order of the lanes, channel r * D/8 + 2 t2 + z at place 16 t2 + 2 r + z, and
-        // rows are padded by 4, so that a store's lanes meet all banks.
-        constexpr int kRow = D + 4;
-        float *wm = reinterpret_cast<float *>(smem);
-        float *wl = wm + kWarps * kRows, *wf = wl + kWarps * kRows;
-        float *wo = wf + kWarps * kRows;
+        // Merge the warps.
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -739,6 +763,8 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
                 const float f2 = ml.y == 0.f ? 0.f : vg / ml.y;
                 store_out(b, h, rho, p4, make_float4(os.x * f2, os.y * f2, os.z * f2, os.w * f2));
                 if (a.lse && p4 == 0) a.lse[orow_of(b, h, rho)] = lse_of(ml.x, ml.y);
+            } else if (!split) {  // over the first warp's own, which this thread alone reads
+                *reinterpret_cast<float4 *>(wo + rho * kRow + 4 * p4) = os;
             } else {
                 reinterpret_cast<float4 *>(a.part_o + ((size_t)slot * kMaxGroup + rho) * D)[p4] = os;
                 if (p4 == 0) a.part_ml[slot * kMaxGroup + rho] = ml;
@@ -750,15 +776,21 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         ustart = uend;
     }
 
-    // Merge the units that span CTAs: behind a grid barrier each of a unit's CTAs takes
-    // an equal share of its (row, four channels) items, with gl lanes an item, a lane a part.
-    if (split && gridDim.x > 1) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) sh_ok = grid_barrier_bounded(a.grid_bar, gridDim.x) ? 1u : 0u;
-        __syncthreads();
-        if (!sh_ok && tid == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
-        __threadfence();
+    // Merge the units that span CTAs: behind a barrier of the grid, or of the cluster, whose
+    // partials are in its shared memory, each of a unit's CTAs takes an equal share of its
+    // (row, four channels) items, with gl lanes an item, a lane a part.
+    if (split ? gridDim.x > 1 : a.cluster > 1) {
+        if (split) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) sh_ok = grid_barrier_bounded(a.grid_bar, gridDim.x) ? 1u : 0u;
+            __syncthreads();
+            if (!sh_ok && tid == 0) set_error(a.err, RESA_DEVERR_TIMEOUT);
+            __threadfence();
+        } else {
+            if (tid == 0) sh_ok = 1u;
+            cg::this_cluster().sync();
+        }
 #pragma unroll 1
         for (int w2 = 0; w2 < 2 && sh_ok; ++w2) {
             const Part pt = sh_part[w2];
@@ -780,9 +812,17 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
                 float4 os = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (int q = me; q < parts; q += gl) {
-                    const size_t at = (size_t)(2 * (q0 + q) + (q == 0 ? odd : 0)) * kMaxGroup + rho;
-                    const float2 ml = __ldcg(a.part_ml + at);
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + p4);
+                    float2 ml;
+                    float4 v;
+                    if (split) {
+                        const size_t at = (size_t)(2 * (q0 + q) + (q == 0 ? odd : 0)) * kMaxGroup + rho;
+                        ml = __ldcg(a.part_ml + at);
+                        v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + at * D) + p4);
+                    } else {
+                        ml = *cg::this_cluster().map_shared_rank(sh_ml + rho, q);
+                        v = *reinterpret_cast<const float4 *>(
+                            cg::this_cluster().map_shared_rank(wo + rho * kRow + 4 * p4, q));
+                    }
                     const float mn = fmaxf(ms, ml.x);
                     const float f1 = mn == -INFINITY ? 0.f : ex2(ms - mn), f2 = mn == -INFINITY ? 0.f : ex2(ml.x - mn);
                     ms = mn;
@@ -816,6 +856,9 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         }
     }
 
+    // no CTA leaves while another reads its shared memory
+    if (!split && a.cluster > 1) cg::this_cluster().sync();
+
     // Units without any block: zeros and -inf, and the errors of every unit.
     for (int u = cta; u < units; u += gridDim.x) {
         if (kept && sh_units[u].x > 0) continue;
@@ -843,10 +886,16 @@ cudaError_t launch_t(const DecodeQ4Args &a, int ctas, cudaStream_t st) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
-    attr[1].val.cooperative = 1;
+    if (a.grid_bar != nullptr) {
+        attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs meet at a grid barrier
+        attr[1].val.cooperative = 1;
+    } else {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = a.cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = a.grid_bar != nullptr && ctas > 1 ? 2 : 1;
+    cfg.numAttrs = (a.grid_bar != nullptr ? ctas : a.cluster) > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, NT>, a);
 }
 
@@ -890,12 +939,22 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
     const long long ctas_most = (most * s.bs + 255) / 256;
     const int all = sms < kNumSms ? sms : kNumSms;
     int ctas = ctas_most < all ? (int)ctas_most : all;
-    // Units short enough for one CTA each: no barrier, no merge, no cooperative launch.
+    // Units short enough for one CTA each, or for a cluster: no grid barrier, no cooperative
+    // launch.
     const long long longest = (block_idx ? (long long)max_topk + 1 : s.max_pages) * s.bs;
     const int units = s.batch * s.hkv;
-    if (longest <= kWholeKeys[rows > 8] || (longest <= kWholeKeysMany && units * 5 >= all * 4)) {
+    a.cluster = 1;
+    const int wide = rows > 8;
+    int cl = 8;
+    while (cl > 1 && units > cluster_units(cl)) cl /= 2;
+    if (longest <= (cl > 1 ? kWholeNear : kWholeKeys)[wide] || (longest <= kWholeKeysMany && units * 5 >= all * 4)) {
         a.grid_bar = nullptr;
         ctas = units;
+    } else if (cl > 1 && longest <= (long long)kClusterKeys[wide] * cl &&
+               longest * (all - units * cl) <= (long long)kClusterMore[wide] * cl * all) {
+        a.grid_bar = nullptr;
+        a.cluster = cl;
+        ctas = units * cl;
     }
     if (s.d == 128) return rows <= 8 ? launch_t<128, 1>(a, ctas, st) : launch_t<128, 2>(a, ctas, st);
     return rows <= 8 ? launch_t<64, 1>(a, ctas, st) : launch_t<64, 2>(a, ctas, st);

@@ -595,6 +595,36 @@ def test_attention_splits(cuda_device, case):
     assert np.array_equal(out, o2) and np.array_equal(lse, l2)
 
 
+CLUSTERS = [  # layout, lens, width of the table in keys, rows a sequence: units of 8, 4 and 2 CTAs
+    ((28, 4, 128, 16), [1, 383, 385, 6001], 6016, 1),
+    ((28, 4, 128, 16), [4000, 2, 17, 400, 1600, 3999, 769], 4000, 1),
+    ((28, 4, 128, 16), [1 + 150 * i for i in range(13)], 2000, 1),
+    ((32, 2, 64, 32), [3, 1500, 4095], 4096, 1),
+    ((32, 2, 64, 32), [2 + 180 * i for i in range(11)], 2048, 1),
+    ((32, 2, 128, 16), [1000 - 31 * i for i in range(30)], 1008, 1),
+    ((8, 8, 64, 64), [5000], 5120, 7),
+    ((14, 2, 128, 16), [2, 2500, 771], 2512, 2),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CLUSTERS)))
+def test_attention_clusters(cuda_device, case):
+    """Units that a thread-block cluster shares, some of its CTAs without a key."""
+    (hq, hkv, d, b), lens, width, f = CLUSTERS[case]
+    p = Problem(161 + case, lens, hq, hkv, d, b, cuda_device, extra_pages=width // b - (-(-max(lens) // b)))
+    q = q4.bf16(p.rng.standard_normal((len(lens), f, hq, d)))
+    tq = torch.from_numpy(q).to(cuda_device).bfloat16()
+    out, lse = chunk(p, f, None, tq)
+    assert p.status() == 0
+    limit = np.repeat(np.arange(f), p.g)
+    for i in sorted({0, 1 % len(lens), len(lens) // 2, len(lens) - 1}):
+        for h in range(hkv):
+            rows = lambda x: x[i, :, h * p.g:(h + 1) * p.g].reshape((-1,) + x.shape[3:])
+            check_rows(p, rows(out), rows(lse), rows(q), i, h, None, lens[i] - f + 1 + limit)
+    o2, l2 = chunk(p, f, None, tq)
+    assert np.array_equal(out, o2) and np.array_equal(lse, l2)
+
+
 @pytest.mark.parametrize("layout,lens,f", [((28, 4, 128, 16), [3000, 130, 900], 40),
                                            ((16, 8, 64, 32), [70 + 40 * i for i in range(24)], 20)],
                          ids=["few", "many"])
