@@ -19,7 +19,7 @@
 // the latency of 24 warps an SM (80 registers) more than by a unit (issue 55 %, exp and
 // sine unit 20 %, fp64 5 %); one token of each of 32 sequences 4.7 us, latency alone.
 // Five ragged prompts of up to 2777 tokens into 4-bit pages (32 / 8 heads, d 128) and the
-// pages' expansion, 189 MB together, take 75 us: the groups' maxima, scales and codes
+// pages' expansion, 189 MB together, take 63 us: the groups' maxima, scales and codes
 // are added to each key and value.
 #include "q4_common.cuh"
 
@@ -368,9 +368,10 @@ __global__ void __launch_bounds__(kThreads, 3)
 // ---------------------------------------------------------------------------
 // 4-bit pages to bf16 pages
 // ---------------------------------------------------------------------------
-constexpr int kExpandTokens = 64;  // positions a CTA expands
+constexpr int kExpandTokens = 64;  // positions a CTA expands, or some of their groups
+constexpr int kExpandAhead = 4;
 
-// Grid (ceil(max positions / kExpandTokens), batch).  A thread turns a group of 16
+// Grid (ceil(max positions / kExpandTokens), batch, parts of their groups).  A thread turns a group of 16
 // channels (8 bytes of codes and a scale) into one 32-byte store, kAhead groups in
 // flight; a warp's reads and writes are contiguous runs.  Measured: 4 x 65536 tokens of 4
 // heads, d 128, 685 MB, 115 us, 6.0 TB/s (16-byte stores, one group in flight: 179 us).
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads)
                      const int32_t *__restrict__ seq_len, uint16_t *__restrict__ k_out,
                      uint16_t *__restrict__ v_out, int lg_hkv, int max_pages, int num_pages, int lg_bs,
                      const RowMap rm, bool wide, uint32_t *err) {
-    constexpr int kAhead = 4, LG = D == 128 ? 3 : 2;  // 2^LG groups a row
+    constexpr int kAhead = kExpandAhead, LG = D == 128 ? 3 : 2;  // 2^LG groups a row
     __shared__ int pages[kExpandTokens / 16];
     pdl_launch_next();
     pdl_wait();
@@ -417,7 +418,7 @@ __global__ void __launch_bounds__(kThreads)
         at = ((size_t)pages[pi] << lg_page) + i;
         return true;
     };
-    for (int e0 = tid; e0 < all; e0 += kAhead * kThreads) {
+    for (int e0 = blockIdx.z * kAhead * kThreads + tid; e0 < all; e0 += gridDim.z * kAhead * kThreads) {
         uint2 w[kAhead];
         uint32_t sf[kAhead];
 #pragma unroll
@@ -488,8 +489,12 @@ cudaError_t launch_append_rope(const Shape &s, const AppendArgs &a, bool q4, uin
 cudaError_t launch_expand_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
                              const int32_t *seq_len, void *k_out, void *v_out, uint32_t *err,
                              cudaStream_t st) {
-    const dim3 grid((unsigned)(((long long)s.max_pages * s.bs + kExpandTokens - 1) / kExpandTokens),
-                    s.batch);
+    // Eight CTAs an SM (five run at once) where there are the groups for it: five sequences of up
+    // to 2888 tokens, 8 heads, d 128, 21.7 us with a CTA for all groups of 64 tokens, 8.6 so.
+    const long long pieces = ((long long)s.max_pages * s.bs + kExpandTokens - 1) / kExpandTokens;
+    const long long lack = (8 * kNumSms - 1) / (pieces * s.batch) + 1;
+    const int rounds = kExpandTokens * s.hkv * (s.d / 16) * 2 / (kExpandAhead * kThreads);
+    const dim3 grid((unsigned)pieces, s.batch, rounds < 1 ? 1 : lack < rounds ? (unsigned)lack : rounds);
     auto kernel = s.d == 128 ? expand_q4_kernel<128> : expand_q4_kernel<64>;
     const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
     auto lg = [](int x) { return x == 1 ? 0 : x == 2 ? 1 : x == 4 ? 2 : x == 8 ? 3 : x == 16 ? 4 : x == 32 ? 5 : 6; };
