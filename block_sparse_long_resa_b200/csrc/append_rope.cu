@@ -3,12 +3,14 @@
 // expansion to bf16 pages (ReSA summary §3.2 "Block Key Cache", Eq. 3;
 // Algorithm 1 incremental updates, for any number of tokens).
 //
-// Grid (key CTAs and token CTAs in turns; batch).  A key CTA owns one block of the
+// Grid (key and token clusters in turns; batch).  A key cluster owns one block of the
 // cache that holds fresh tokens and a range of kv heads, so it alone writes that
-// block's keys and its descriptor: 16 tokens at a time it brings the keys as stored
+// block's keys and its descriptor.  Each of its CTAs brings 16 tokens' keys as stored
 // (rotated, or read back from the cache below the first fresh slot) into shared
-// memory and folds their min / max per channel.  Of a token CTA a warp, or several
-// where there are few tokens, takes a token: its queries and its values.
+// memory and folds their min / max per channel, and through the cluster's shared memory
+// they fold the block's (with one CTA for the four tiles of a 64-token block five prompts
+// took 55 us, not 48).  Of a token CTA a warp, or several where there are few tokens,
+// takes a token: its queries and its values.
 //
 // An angle is pos * inv_freq in turns in fp64, reduced to [-1/2, 1/2] before
 // the sine, so that a position of 2^20 has as good an angle as position 1.  Keys
@@ -19,9 +21,13 @@
 // the latency of 24 warps an SM (80 registers) more than by a unit (issue 55 %, exp and
 // sine unit 20 %, fp64 5 %); one token of each of 32 sequences 4.7 us, latency alone.
 // Five ragged prompts of up to 2777 tokens into 4-bit pages (32 / 8 heads, d 128) and the
-// pages' expansion, 189 MB together, take 63 us: the groups' maxima, scales and codes
+// pages' expansion, 189 MB together, take 57 us: the groups' maxima, scales and codes
 // are added to each key and value.
+#include <cooperative_groups.h>
+
 #include "q4_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace resa {
 namespace {
@@ -33,7 +39,7 @@ constexpr double kInvTwoPi = 0.15915494309189533577;
 struct AppendGeom {
     int hq, hkv, lg_heads;  // 2^lg_heads kv heads a key CTA takes
     int max_pages, num_pages, bs;
-    int key_ctas;        // CTAs of keys along x
+    int key_clusters;    // clusters of keys along x
     int q_tokens;        // tokens a token CTA takes: 1, 2, 4 or 8
     RowMap rm;
 };
@@ -150,14 +156,16 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int start = L - n;  // cache position of the first fresh token
     const int half = a.rot / 2;
 
-    // Key and token CTAs take turns along x, so that they share the SMs.
-    const int ctas = gridDim.x;
-    const int ki = (int)((long long)blockIdx.x * gm.key_ctas / ctas);
+    // Key and token clusters, of a CTA for each tile of a block, take turns along x, so that
+    // they share the SMs.
+    const int tiles = gm.bs / kTileRows, clusters = gridDim.x / tiles;
+    const int cluster = blockIdx.x / tiles, rank = blockIdx.x % tiles;
+    const int ki = (int)((long long)cluster * gm.key_clusters / clusters);
     bool bad = false;
-    if ((int)(((long long)blockIdx.x + 1) * gm.key_ctas / ctas) == ki) {  // ---- a token's queries and values
+    if ((int)(((long long)cluster + 1) * gm.key_clusters / clusters) == ki) {  // ---- a token's queries and values
         // warps per token: 8 / q_tokens, each a share of the vectors
         const int wpt = kWarps / gm.q_tokens, step = 32 * wpt;
-        const int r = ((int)blockIdx.x - ki) * gm.q_tokens + warp / wpt;
+        const int r = ((cluster - ki) * tiles + rank) * gm.q_tokens + warp / wpt;
         if (r >= n) return;
         const size_t tok = (size_t)b * a.f + r;
         const int pos = start + r;
@@ -245,123 +253,121 @@ __global__ void __launch_bounds__(kThreads, 3)
     const size_t prow = (size_t)page * gm.hkv + h0;  // (page, head) row base
     const int lg_row = gm.lg_heads + (D == 128 ? 3 : 2);  // slots of a token: 2^lg_row
     const Slot sl = slot_of<D>(tid % SPR, a.rot, a.interleaved);
-    constexpr int kFold = kMaxKvHeads * (D / 2) / kThreads;  // channel pairs a thread folds
-    uint32_t mn[kFold], mx[kFold];
+    const int t0 = rank * kTileRows;                 // the first of this CTA's tile
+    const int nt = max(0, min(kTileRows, valid - t0));
+    const int old = max(0, min(nt, fresh0 - t0));                   // keys that are there already
+    const int nf = nt - old;
+    const int r0 = pos0 + t0 + old - start;                         // the first fresh one's row
+    const int slots = nf << lg_row;
+    auto src_of = [&](int e) -> const uint4 * {
+        return reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) +
+                                               ((size_t)b * a.f + r0 + (e >> lg_row)) * a.k_stride +
+                                               (size_t)(h0 + (e / SPR & (heads - 1))) * D);
+    };
+    // a thread's first vectors are on their way while the angles are worked out
+    constexpr int kAhead = 2;
+    uint4 x1[kAhead], x2[kAhead];
 #pragma unroll
-    for (int j = 0; j < kFold; ++j) mn[j] = mx[j] = 0u;
-
-#pragma unroll 1
-    for (int t0 = 0; t0 < valid; t0 += kTileRows) {
-        const int nt = min(kTileRows, valid - t0);
-        const int old = max(0, min(nt, fresh0 - t0));                   // keys that are there already
-        const int nf = nt - old;
-        const int r0 = pos0 + t0 + old - start;                         // the first fresh one's row
-        const int slots = nf << lg_row;
-        auto src_of = [&](int e) -> const uint4 * {
-            return reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.kn) +
-                                                   ((size_t)b * a.f + r0 + (e >> lg_row)) * a.k_stride +
-                                                   (size_t)(h0 + (e / SPR & (heads - 1))) * D);
-        };
-        // a thread's first vectors are on their way while the angles are worked out
-        constexpr int kAhead = 2;
-        uint4 x1[kAhead], x2[kAhead];
+    for (int k = 0; k < kAhead; ++k)
+        if (tid + k * kThreads < slots) {
+            const uint4 *src = src_of(tid + k * kThreads);
+            x1[k] = src[sl.c1];
+            x2[k] = src[sl.c2];
+        }
+#pragma unroll 2
+    for (int e = tid; e < nf * half; e += kThreads) {
+        const int t = e / half, i = e - t * half;
+        double s, c;
+        sincospi(2.0 * turns(a, b, r0 + t, start + r0 + t, i), &s, &c);
+        tab[t * (D / 2) + (i ^ (i / 8 % 8))] = make_double2(c * a.mscale, s * a.mscale);
+    }
+    for (int e = tid; e < old * heads * CPR; e += kThreads) {
+        const int c = e % CPR, th = e / CPR;
+        const int h = th & (heads - 1), t = t0 + (th >> gm.lg_heads);
+        const size_t slot = (prow + h) * gm.bs + t;
+        if (Q4) {
+            const uint32_t w = static_cast<const uint32_t *>(a.k)[slot * CPR + c];
+            const uint32_t sf = static_cast<const uint8_t *>(a.k_sf)[slot * SPR + c / 2];
+            keys[e] = q4_values_bf16(w, sf, head_scale(a.k_scale, h0 + h));
+        } else {
+            keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
+        }
+    }
+    __syncthreads();
+    for (int e0 = tid; e0 < slots; e0 += kAhead * kThreads) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (tid + k * kThreads < slots) {
-                const uint4 *src = src_of(tid + k * kThreads);
+        for (int k = 0; k < kAhead; ++k) {
+            const int e = e0 + k * kThreads;
+            if (e >= slots) break;
+            if (e0 != tid) {
+                const uint4 *src = src_of(e);
                 x1[k] = src[sl.c1];
                 x2[k] = src[sl.c2];
             }
-        if (t0) __syncthreads();
-#pragma unroll 2
-        for (int e = tid; e < nf * half; e += kThreads) {
-            const int t = e / half, i = e - t * half;
-            double s, c;
-            sincospi(2.0 * turns(a, b, r0 + t, start + r0 + t, i), &s, &c);
-            tab[t * (D / 2) + (i ^ (i / 8 % 8))] = make_double2(c * a.mscale, s * a.mscale);
-        }
-        for (int e = tid; e < old * heads * CPR; e += kThreads) {
-            const int c = e % CPR, th = e / CPR;
-            const int h = th & (heads - 1), t = t0 + (th >> gm.lg_heads);
-            const size_t slot = (prow + h) * gm.bs + t;
-            if (Q4) {
-                const uint32_t w = static_cast<const uint32_t *>(a.k)[slot * CPR + c];
-                const uint32_t sf = static_cast<const uint8_t *>(a.k_sf)[slot * SPR + c / 2];
-                keys[e] = q4_values_bf16(w, sf, head_scale(a.k_scale, h0 + h));
-            } else {
-                keys[e] = static_cast<const uint4 *>(a.k)[slot * CPR + c];
+            const int t = e >> lg_row, h = e / SPR & (heads - 1);
+            double2 cs[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int f = (i < 4 ? sl.f1 : sl.f2 - 4) + i;
+                cs[i] = tab[t * (D / 2) + (f ^ (f / 8 % 8))];
             }
+            rotate_slot<double>(x1[k], x2[k], sl, a.interleaved, cs);
+            uint4 *dst = keys + ((old + t) * heads + h) * CPR;
+            dst[sl.c1] = x1[k];
+            dst[sl.c2] = x2[k];
+            if (!Q4) {
+                uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + t0 + old + t) * CPR;
+                out[sl.c1] = x1[k];
+                out[sl.c2] = x2[k];
+            }
+        }
+    }
+    __syncthreads();
+    if (Q4) {
+        // 4-bit codes of the fresh keys; shared memory then holds what they stand for
+        for (int e = tid; e < slots; e += kThreads) {
+            const int gi = e % SPR, h = e / SPR & (heads - 1), t = old + (e >> lg_row);
+            uint4 *kp = keys + (t * heads + h) * CPR + 2 * gi;
+            const uint4 y0 = kp[0], y1 = kp[1];
+            const uint32_t w[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+            const float g = head_scale(a.k_scale, h0 + h);
+            uint2 codes;
+            uint32_t sf;
+            bad |= q4_quantise(w, 1.f / g, codes, sf);
+            const size_t at = ((prow + h) * gm.bs + t0 + t) * SPR + gi;
+            static_cast<uint2 *>(a.k)[at] = codes;
+            static_cast<uint8_t *>(a.k_sf)[at] = (uint8_t)sf;
+            kp[0] = q4_values_bf16(codes.x, sf, g);
+            kp[1] = q4_values_bf16(codes.y, sf, g);
         }
         __syncthreads();
-        for (int e0 = tid; e0 < slots; e0 += kAhead * kThreads) {
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int e = e0 + k * kThreads;
-                if (e >= slots) break;
-                if (e0 != tid) {
-                    const uint4 *src = src_of(e);
-                    x1[k] = src[sl.c1];
-                    x2[k] = src[sl.c2];
-                }
-                const int t = e >> lg_row, h = e / SPR & (heads - 1);
-                double2 cs[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int f = (i < 4 ? sl.f1 : sl.f2 - 4) + i;
-                    cs[i] = tab[t * (D / 2) + (f ^ (f / 8 % 8))];
-                }
-                rotate_slot<double>(x1[k], x2[k], sl, a.interleaved, cs);
-                uint4 *dst = keys + ((old + t) * heads + h) * CPR;
-                dst[sl.c1] = x1[k];
-                dst[sl.c2] = x2[k];
-                if (!Q4) {
-                    uint4 *out = static_cast<uint4 *>(a.k) + ((prow + h) * gm.bs + t0 + old + t) * CPR;
-                    out[sl.c1] = x1[k];
-                    out[sl.c2] = x2[k];
-                }
-            }
-        }
-        __syncthreads();
-        if (Q4) {
-            // 4-bit codes of the fresh keys; shared memory then holds what they stand for
-            for (int e = tid; e < slots; e += kThreads) {
-                const int gi = e % SPR, h = e / SPR & (heads - 1), t = old + (e >> lg_row);
-                uint4 *kp = keys + (t * heads + h) * CPR + 2 * gi;
-                const uint4 y0 = kp[0], y1 = kp[1];
-                const uint32_t w[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-                const float g = head_scale(a.k_scale, h0 + h);
-                uint2 codes;
-                uint32_t sf;
-                bad |= q4_quantise(w, 1.f / g, codes, sf);
-                const size_t at = ((prow + h) * gm.bs + t0 + t) * SPR + gi;
-                static_cast<uint2 *>(a.k)[at] = codes;
-                static_cast<uint8_t *>(a.k_sf)[at] = (uint8_t)sf;
-                kp[0] = q4_values_bf16(codes.x, sf, g);
-                kp[1] = q4_values_bf16(codes.y, sf, g);
-            }
-            __syncthreads();
-        }
-        // descriptors: a thread two channels of a head
-        const uint32_t *kw = reinterpret_cast<const uint32_t *>(keys);
-#pragma unroll
-        for (int j = 0; j < kFold; ++j) {
-            const int e = tid + j * kThreads, width = heads * (D / 2);
-            if (e < width) {
-                if (t0 == 0) mn[j] = mx[j] = kw[e];
+    }
+    // Descriptors: a thread two channels of a head, from the neutral values in all tiles but the
+    // block's first; then each CTA a share of the channels over the tiles, in order.
+    const uint32_t *kw = reinterpret_cast<const uint32_t *>(keys);
+    uint2 *fold = reinterpret_cast<uint2 *>(tab);  // (the angles are used up)
+    const int width = heads * (D / 2);
+    for (int e = tid; e < width; e += kThreads) {
+        uint32_t mn = rank == 0 ? kw[e] : 0x7f807f80u, mx = rank == 0 ? kw[e] : 0xff80ff80u;
 #pragma unroll 4
-                for (int t = t0 == 0; t < nt; ++t) fold2(mn[j], mx[j], kw[t * width + e]);
-            }
-        }
+        for (int t = rank == 0; t < nt; ++t) fold2(mn, mx, kw[t * width + e]);
+        fold[e] = make_uint2(mn, mx);
     }
-#pragma unroll
-    for (int j = 0; j < kFold; ++j) {
-        const int e = tid + j * kThreads;
-        if (e < heads * (D / 2)) {
-            uint32_t *d = static_cast<uint32_t *>(a.desc) + (prow + e / (D / 2)) * D + e % (D / 2);  // [2][D / 2] words
-            d[0] = mn[j];
-            d[D / 2] = mx[j];
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int e = width * rank / tiles + tid; e < width * (rank + 1) / tiles; e += kThreads) {
+        uint2 m = *cl.map_shared_rank(fold + e, 0);
+        for (int q = 1; q < tiles; ++q) {
+            const uint2 x = *cl.map_shared_rank(fold + e, q);
+            uint32_t other = 0u;
+            fold2(m.x, other, x.x);
+            fold2(other, m.y, x.y);
         }
+        uint32_t *d = static_cast<uint32_t *>(a.desc) + (prow + e / (D / 2)) * D + e % (D / 2);  // [2][D / 2] words
+        d[0] = m.x;
+        d[D / 2] = m.y;
     }
+    if (tiles > 1) cl.sync();  // no CTA leaves while another reads its shared memory
     if (Q4 && bad) set_error(err, RESA_DEVERR_NONFINITE);
 }
 
@@ -466,14 +472,27 @@ cudaError_t launch_append_t(const Shape &s, const AppendArgs &a, uint32_t *err, 
     if (blocks > s.max_pages) blocks = s.max_pages;
     // All heads a CTA, so that the angles are worked out once, unless that leaves too few CTAs.
     int lg_heads = s.hkv == 8 ? 3 : s.hkv == 4 ? 2 : s.hkv == 2 ? 1 : 0;
-    while (lg_heads > 0 && blocks * s.batch * (s.hkv >> lg_heads) < 2 * kNumSms) --lg_heads;
+    const int tiles = s.bs / kTileRows;
+    while (lg_heads > 0 && blocks * tiles * s.batch * (s.hkv >> lg_heads) < 2 * kNumSms) --lg_heads;
     gm.lg_heads = lg_heads;
-    gm.key_ctas = (int)blocks * (s.hkv >> lg_heads);
+    gm.key_clusters = (int)blocks * (s.hkv >> lg_heads);
     gm.q_tokens = a.f >= kWarps ? kWarps : a.f >= 4 ? 4 : a.f >= 2 ? 2 : 1;
-    const int token_ctas = (a.f - 1) / gm.q_tokens + 1;
+    const int token_clusters = ((a.f - 1) / gm.q_tokens + tiles) / tiles;
     const int smem = (kTileRows * D * 2 << lg_heads) + kTileRows * (D / 2) * 16;  // at most 48 KB
-    return launch_pdl(append_rope_kernel<D, Q4>, dim3(gm.key_ctas + token_ctas, s.batch),
-                      dim3(kThreads), smem, st, a, gm, err);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((gm.key_clusters + token_clusters) * tiles, s.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = tiles;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = tiles > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, append_rope_kernel<D, Q4>, a, gm, err);
 }
 
 }  // namespace
