@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from block_sparse_long_resa_b200 import resa as R
+from block_sparse_long_resa_b200.cache import workspace as R_workspace
 from oracle import q4
 from q4_problem import Problem, attention_tolerance, f64
 
@@ -574,6 +575,8 @@ SPLITS = [  # layout, lens, width of the table in keys: whole units, even shares
     ((16, 8, 128, 16), [1 + 7 * i for i in range(40)], 40000),       # more units than SMs
     ((8, 8, 64, 64), [3000] + [2 + i for i in range(17)], 40000),    # one long unit among short ones
     ((14, 2, 128, 16), [20000, 1, 19999], 20100),
+    ((16, 8, 64, 32), [1 + 9 * i for i in range(60)], 9600),         # more units than threads
+    ((32, 2, 64, 16), [900 - 6 * i for i in range(140)], 9600),
 ]
 
 
@@ -740,3 +743,42 @@ def test_layer_cache_q4_from_nothing(cuda_device):
                                               q4.values(vc, vs), [50, 50], 0.125)
             tol, _ = attention_tolerance(mag[:, None], 50, w, vsum)
             assert (np.abs(f64(a)[i, 2 * h:2 * h + 2] - o) <= tol).all()
+
+
+def test_pages_past_four_gigabytes(cuda_device):
+    """Byte offsets past 32 bits (and element offsets, in the bf16 pages): the last pages of large
+    pools hold what the pages of small ones do."""
+    dev = cuda_device
+    hq, hkv, d, b, f = 16, 8, 128, 64, 130
+    lens = torch.tensor([200, 130], dtype=torch.int32, device=dev)
+    torch.manual_seed(77)
+    q, k, v = (torch.randn(2, f, h, d, device=dev).bfloat16() for h in (hq, hkv, hkv))
+    q1 = torch.randn(2, hq, d, device=dev).bfloat16()
+    inv = torch.tensor(1e4 ** (-np.arange(0, d, 2) / d), dtype=torch.float32, device=dev)
+    idx = torch.tensor([[[3, 0]] * hkv, [[1, 2]] * hkv], dtype=torch.int32, device=dev)
+    cnt = torch.full((2, hkv), 2, dtype=torch.int32, device=dev)
+    cfg, got = R.make_config(hq, hkv, d, b), []
+    for pages in (8, 132000):                                    # 32 KB of codes a page: 4.3 GB
+        p4 = [torch.zeros(pages, hkv, b, d // 2, dtype=torch.uint8, device=dev) for _ in range(2)]
+        sf = [torch.zeros(pages, hkv, b, d // 16, dtype=torch.uint8, device=dev) for _ in range(2)]
+        p16 = [torch.zeros(pages, hkv, b, d, dtype=torch.bfloat16, device=dev) for _ in range(4)]
+        desc = [torch.zeros(pages, hkv, 2, d, dtype=torch.bfloat16, device=dev) for _ in range(2)]
+        table = (pages - 1 - torch.arange(8, dtype=torch.int32, device=dev)).view(2, 4).contiguous()
+        ws = R_workspace(cfg, 2, 4, f, dev)
+        c4 = R.make_cache_q4(p4[0], sf[0], p4[1], sf[1], desc[0], table, lens)
+        c16 = R.make_cache(p16[0], p16[1], desc[1], table, lens)
+        rope, toks = R.make_rope(d, inv), R.make_tokens(q, k, v)
+        qa, qb = torch.zeros_like(q), torch.zeros_like(q)
+        R.resa_append_rope_q4(cfg, c4, rope, toks, qa, ws)
+        R.resa_append_rope(cfg, c16, rope, toks, qb, ws)
+        R.resa_expand_q4(cfg, c4, p16[2], p16[3], ws)
+        o, o1, o2 = (torch.zeros(2, n, hq, d, device=dev) for n in (f, 1, 1))
+        R.resa_attention_q4(cfg, c4, f, None, qa, o, None, ws)
+        R.resa_attention_q4(cfg, c4, 1, None, q1, o1, None, ws)
+        R.resa_sparse_decode_q4(cfg, c4, q1, idx, cnt, 1, o2, None, ws)
+        assert R.resa_check_device_status(ws, raise_on_error=False) == 0
+        got.append([x[pages - 8:].clone() for x in p4 + sf + p16 + desc] + [qa, qb, o, o1, o2])
+        del p4, sf, p16, desc, c4, c16
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert all(x.abs().float().max() > 0 for x in got[0])
