@@ -859,8 +859,10 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
     // no CTA leaves while another reads its shared memory
     if (!split && a.cluster > 1) cg::this_cluster().sync();
 
-    // Units without any block: zeros and -inf, and the errors of every unit.
-    for (int u = cta; u < units; u += gridDim.x) {
+    // Units without any block: zeros and -inf, and the errors of every unit.  (A unit's loads again
+    // only where it may be one: they would take 1 us after the merge.)
+    const int u0 = split ? cta : own == 0 && own_first == cta ? cta / a.cluster : units;
+    for (int u = u0; u < units; u += split ? gridDim.x : units) {
         if (kept && sh_units[u].x > 0) continue;
         const Unit x = unit_of(u, tid == 0);
         if (x.cnt > 0 || !x.live) continue;
