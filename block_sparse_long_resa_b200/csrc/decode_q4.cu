@@ -151,8 +151,11 @@ struct Unit {
     bool live;                 // outputs are written (else they stay as they were)
 };
 
-struct Part {
-    int b, h, rows, ustart, uend;  // rows 0: none
+struct Part {  // rows 0: none
+    int b, h, rows;
+    int q0, parts, odd;  // CTAs q0 .. whose shares meet the unit; odd: q0's is its later piece
+    int i0, i1;          // the items this CTA merges
+    float vg;
 };
 
 struct DecodeQ4Args {
@@ -770,7 +773,18 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
                 if (p4 == 0) a.part_ml[slot * kMaxGroup + rho] = ml;
             }
         }
-        if (!whole && tid == 0) sh_part[x == x0 ? 0 : 1] = Part{b, h, rows_all, ustart, uend};
+        if (!whole && tid == 32) {  // what the merge wants to know, worked out before the barrier
+            Part pt{b, h, rows_all, own_first, own, 0, 0, 0, vg};
+            if (own == 0) {  // only q0's share can begin before the unit
+                pt.q0 = (int)((((long long)ustart + 1) * G - 1) / W);
+                pt.parts = (int)(((long long)uend * G - 1) / W) - pt.q0 + 1;
+                pt.odd = entry_of(pt.q0) < ustart ? 1 : 0;
+            }
+            const int items = rows_all * (D / 4);
+            pt.i0 = items * (cta - pt.q0) / pt.parts;
+            pt.i1 = items * (cta - pt.q0 + 1) / pt.parts;
+            sh_part[x == x0 ? 0 : 1] = pt;
+        }
         __syncthreads();  // the merge area is the ring again
         x = min(x1, uend);
         ustart = uend;
@@ -795,15 +809,9 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         for (int w2 = 0; w2 < 2 && sh_ok; ++w2) {
             const Part pt = sh_part[w2];
             if (pt.rows == 0) continue;
-            // CTAs q0 .. q1 whose shares meet the unit; only q0's can begin before it
-            const int q0 = own > 0 ? own_first : (int)((((long long)pt.ustart + 1) * G - 1) / W);
-            const int q1 = own > 0 ? q0 + own - 1 : (int)(((long long)pt.uend * G - 1) / W);
-            const int parts = q1 - q0 + 1, odd = own == 0 && entry_of(q0) < pt.ustart ? 1 : 0;
-            const int items = pt.rows * (D / 4);
-            const int i0 = items * (cta - q0) / parts, i1 = items * (cta - q0 + 1) / parts;
+            const int q0 = pt.q0, parts = pt.parts, odd = pt.odd, i0 = pt.i0, i1 = pt.i1;
             const int lg = parts > 16 ? 5 : parts > 8 ? 4 : parts > 4 ? 3 : parts > 2 ? 2 : 1;
             const int gl = 1 << lg, me = tid & (gl - 1);
-            const float vg = head_scale(a.c.v_scale, pt.h);
 #pragma unroll 1
             for (int base = i0; base < i1; base += kThreads >> lg) {
                 const int e = base + (tid >> lg);
@@ -848,7 +856,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
                     os.w += __shfl_xor_sync(0xffffffffu, os.w, o2);
                 }
                 if (me == 0 && e < i1) {
-                    const float f2 = ls == 0.f ? 0.f : vg / ls;
+                    const float f2 = ls == 0.f ? 0.f : pt.vg / ls;
                     store_out(pt.b, pt.h, rho, p4, make_float4(os.x * f2, os.y * f2, os.z * f2, os.w * f2));
                     if (a.lse && p4 == 0) a.lse[orow_of(pt.b, pt.h, rho)] = lse_of(mt, ls);
                 }
