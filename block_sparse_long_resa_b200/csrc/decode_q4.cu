@@ -124,6 +124,13 @@ __device__ __forceinline__ uint32_t v_chunk(int t, int chunk) {
 __device__ __forceinline__ void cp_async16_s(uint32_t smem_dst, const void *gsrc) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
 }
+// A load that stays where it is among the asynchronous copies.
+__device__ __forceinline__ uint4 ld_now(const uint4 *p) {
+    uint4 x;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p) : "memory");
+    return x;
+}
 // Shared-memory loads of 1, 2 or 4 consecutive words, and of a byte or two.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
@@ -446,14 +453,10 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             }
             cp_async_commit();
         };
-#pragma unroll
-        for (int t = 0; t < kStages - 1; ++t) issue(t);
-
-        // Q^T fragments and each row's factors.
-        uint32_t qb[D / 16][NT][2];
-        float row_scale[NT][2];
-        int lim[NT][2];  // positions row 2c + k of n-tile n sees (0: no such row)
-        const float kg = head_scale(a.c.k_scale, h);
+        // The queries and the head's scales are asked for first: behind the rings' first copies
+        // they took 3 us.
+        const float kg = head_scale(a.c.k_scale, h), vg = head_scale(a.c.v_scale, h);
+        uint4 qx[NT][D / 32];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int rho = n * 8 + r;
@@ -461,11 +464,22 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             const int qr = ok ? rho : 0;
             const size_t qrow = ((size_t)b * a.f + qr / a.g) * a.hq + (size_t)h * a.g + qr % a.g;
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + qrow * D + c * (D / 4));
-            uint4 x[D / 32];
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) qx[n][i] = ok ? ld_now(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int t = 0; t < kStages - 1; ++t) issue(t);
+
+        // Q^T fragments and each row's factors.
+        uint32_t qb[D / 16][NT][2];
+        float row_scale[NT][2];
+        int lim[NT][2];  // positions row 2c + k of n-tile n sees (0: no such row)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint4(&x)[D / 32] = qx[n];
             uint32_t mag = 0;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
-                x[i] = ok ? src[i] : make_uint4(0u, 0u, 0u, 0u);
                 mag = __vmaxu2(mag, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
                                              __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
             }
@@ -746,7 +760,6 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         }
         __syncthreads();
         const bool whole = j0 == 0 && j1 == un.cnt;
-        const float vg = head_scale(a.c.v_scale, h);
         // Partial slot of this CTA: 2 cta for its first piece, 2 cta + 1 for a later one.
         const int slot = 2 * cta + (x == x0 ? 0 : 1);
         for (int e = tid; e < rows_all * (D / 4); e += kThreads) {
