@@ -31,7 +31,7 @@
 // products start from zero and join the row in fp32 registers (see below).
 //
 // Measured (28 q / 4 kv heads, d 128): every position of one 262144-token sequence,
-// 151 MB, 52 us, 2.9 TB/s.  Instructions bound it: a warp's step of 32 tokens is
+// 151 MB, 51 us, 2.9 TB/s.  Instructions bound it: a warp's step of 32 tokens is
 // about 800 of them, issued at 2 a cycle and SM in 35 us; the rest is the first loads,
 // the barrier and the merge.  16 warps for 12 and two accumulator chains for one
 // changed nothing.  A list of 10 % of the same sequence's blocks, 15 MB: 16 us, nearly
