@@ -782,3 +782,45 @@ def test_pages_past_four_gigabytes(cuda_device):
     for x, y in zip(*got):
         assert torch.equal(x, y)
     assert all(x.abs().float().max() > 0 for x in got[0])
+
+
+@pytest.mark.parametrize("width", [512, 2000, 40000], ids=["whole", "cluster", "grid"])
+def test_captured_decode_with_a_bad_sequence(cuda_device, width):
+    """Every way of sharing units out, captured and replayed: a sequence whose length is out of
+    range is reported and skipped (dense) or zeroed (sparse), the others keep their results."""
+    dev = cuda_device
+    p = Problem(78, [500, 37, 400], 28, 4, 128, 16, dev, extra_pages=width // 16 - 32)
+    q = torch.randn(3, 28, 128, device=dev).bfloat16()
+    lens = p.t_len.clone()
+    most = width // 16 - 1
+    idx = torch.arange(most + 1, dtype=torch.int32, device=dev).expand(3, 4, most + 1).contiguous()
+    cnt = torch.tensor([[32] * 4, [3] * 4, [25] * 4], dtype=torch.int32, device=dev)
+    c4 = p.cache4(seq_len=lens)
+    a, b = torch.zeros(3, 28, 128, device=dev), torch.zeros(3, 28, 128, device=dev)
+    za, zb = torch.zeros(3, 28, device=dev), torch.zeros(3, 28, device=dev)
+
+    def calls():
+        R.resa_attention_q4(p.cfg, c4, 1, None, q, a, za, p.ws)
+        R.resa_sparse_decode_q4(p.cfg, c4, q, idx, cnt, most, b, zb, p.ws)
+
+    calls()
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(za, zb) and p.status() == 0
+    want, wantz = a.clone(), za.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    lens[1] = -1
+    for x in (a, b, za, zb):
+        x.fill_(7.0)
+    g.replay()
+    assert p.status() & 0x1f != 0
+    for got, z, at_bad, z_bad in ((a, za, 7.0, 7.0), (b, zb, 0.0, -np.inf)):
+        for i in (0, 2):
+            assert torch.equal(got[i], want[i]) and torch.equal(z[i], wantz[i])
+        assert (got[1] == at_bad).all() and (z[1] == z_bad).all()
+    R.resa_workspace_init(p.ws)
+    lens[1] = 37
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want) and p.status() == 0
