@@ -168,25 +168,25 @@ def make_config(num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: 
     return resa_config_t(num_q_heads, num_kv_heads, head_dim, block_size, sm_scale)
 
 
+def _keep(struct, *tensors):
+    """The struct holds addresses only: keep these tensors alive with it."""
+    struct.tensors = tensors
+    return struct
+
+
 def make_cache(k, v, desc, page_table, seq_len, rows=None) -> resa_cache_t:
     """Cache struct over torch tensors k/v [pages][Hkv][b][d] bf16, desc
     [pages][Hkv][2][d] bf16, page_table [B][max_pages] int32, seq_len [B] int32.
 
     With ``rows`` (int32 device tensor [n]) the call covers the n sequences in
-    those rows of page_table / seq_len (the row map of resa_cache_t)."""
+    those rows of page_table / seq_len (the row map of resa_cache_t).  The struct
+    keeps page_table, seq_len and rows alive; the pages are the caller's to keep."""
     nrows = int(page_table.shape[0])
-    if rows is None:
-        return resa_cache_t(_ptr(k), _ptr(v), _ptr(desc), _ptr(page_table), _ptr(seq_len),
-                            nrows, int(page_table.shape[1]), int(k.shape[0]), None, 0)
-    return resa_cache_t(_ptr(k), _ptr(v), _ptr(desc), _ptr(page_table), _ptr(seq_len),
-                        int(rows.numel()), int(page_table.shape[1]), int(k.shape[0]),
-                        _ptr(rows), nrows)
-
-
-def _keep(struct, *tensors):
-    """The struct holds addresses only: keep its small tensors alive with it."""
-    struct.tensors = tensors
-    return struct
+    return _keep(resa_cache_t(_ptr(k), _ptr(v), _ptr(desc), _ptr(page_table), _ptr(seq_len),
+                              nrows if rows is None else int(rows.numel()),
+                              int(page_table.shape[1]), int(k.shape[0]), _ptr(rows),
+                              0 if rows is None else nrows),
+                 page_table, seq_len, rows)
 
 
 def _expect(name: str, t, dtype: str, shape=None):
@@ -205,7 +205,8 @@ def make_cache_q4(k, k_sf, v, v_sf, desc, page_table, seq_len, rows=None, k_scal
                   v_scale=None) -> resa_cache_q4_t:
     """4-bit cache struct over torch tensors k/v [pages][Hkv][b][d/2] uint8 codes, k_sf/v_sf
     [pages][Hkv][b][d/16] float8_e4m3fn group scales, desc / page_table / seq_len / rows as in
-    make_cache, and the heads' scales k_scale/v_scale [Hkv] fp32 (None: 1)."""
+    make_cache, and the heads' scales k_scale/v_scale [Hkv] fp32 (None: 1).  The struct keeps
+    all of them alive."""
     pages, hkv, b, half = k.shape
     for name, t, dtype, shape in (
             ("k", k, "uint8", None), ("v", v, "uint8", k.shape),
@@ -222,7 +223,7 @@ def make_cache_q4(k, k_sf, v, v_sf, desc, page_table, seq_len, rows=None, k_scal
                                  nrows if rows is None else int(rows.numel()),
                                  int(page_table.shape[1]), int(k.shape[0]), _ptr(rows),
                                  0 if rows is None else nrows, _ptr(k_scale), _ptr(v_scale)),
-                 rows, k_scale, v_scale)
+                 k, k_sf, v, v_sf, desc, page_table, seq_len, rows, k_scale, v_scale)
 
 
 def make_rope(rot_dim: int, inv_freq, interleaved: bool = False,
