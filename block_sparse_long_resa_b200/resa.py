@@ -255,6 +255,8 @@ def make_tokens(q, k, v, n_new=None, positions=None) -> resa_tokens_t:
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t is not None and (str(t.dtype) != "torch.bfloat16" or tuple(t.shape[:2]) != (b, f)):
             raise ResaError(2, f"make_tokens: {name} is not [batch][f][heads][d] bf16 as k is")
+    if v.shape != k.shape or (q is not None and q.shape[3:] != k.shape[3:]):
+        raise ResaError(2, "make_tokens: v has not k's heads, or the heads differ in size")
     _expect("make_tokens: n_new", n_new, "int32", (b,))
     _expect("make_tokens: positions", positions, "int32", (b, f))
     return _keep(resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),

@@ -2,6 +2,7 @@
 import gc
 import weakref
 
+import pytest
 import torch
 
 from block_sparse_long_resa_b200 import resa as R
@@ -32,3 +33,15 @@ def test_structs_keep_their_lengths_and_tables():
     del args
     gc.collect()
     assert all(x() is not None for x in seen)
+
+
+def test_tokens_of_unlike_heads_are_refused():
+    """k and v of other head counts, or heads of other sizes, would be read past their ends."""
+    x = lambda h, d: torch.zeros(2, 5, h, d, dtype=torch.bfloat16)
+    R.make_tokens(x(8, 64), x(2, 64), x(2, 64))
+    for q, k, v in ((None, x(2, 64), x(1, 64)), (None, x(2, 64), x(4, 64)), (None, x(2, 128), x(2, 64)),
+                    (None, x(2, 64), x(2, 128)), (x(8, 128), x(2, 64), x(2, 64)),
+                    (x(8, 64), x(2, 128), x(2, 128))):
+        with pytest.raises(R.ResaError) as e:
+            R.make_tokens(q, k, v)
+        assert e.value.status == 2
