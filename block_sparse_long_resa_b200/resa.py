@@ -44,6 +44,7 @@ class resa_cache_t(ctypes.Structure):
                 ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("rows", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int32)]
+    device, tensors = None, ()  # as make_cache sets them: index of the tensors' device
 
 
 class resa_cache_q4_t(ctypes.Structure):
@@ -54,11 +55,13 @@ class resa_cache_q4_t(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("rows", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p)]
+    device = None  # index of the tensors' device; None: made of addresses
 
 
 class resa_rope_t(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("inv_freq", ctypes.c_void_p), ("mscale", ctypes.c_float)]
+    device = None
 
 
 class resa_tokens_t(ctypes.Structure):
@@ -66,6 +69,7 @@ class resa_tokens_t(ctypes.Structure):
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("v_stride", ctypes.c_int64), ("f", ctypes.c_int32),
                 ("n_new", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+    device = None
 
 
 _lib = None
@@ -142,16 +146,51 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
-def _stream_at(stream, ws, where: str) -> Optional[int]:
-    """_stream, of a call whose workspace has to be on the current device."""
-    if stream is not None:
-        return _stream(stream)
-    if ws.device.type != "cuda":
+def _device(where: str, tensors) -> Optional[int]:
+    """Device index (-1: host memory) of the tensors among these; None when there are only
+    addresses, which are the caller's to vouch for."""
+    dev = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ResaError(4, f"{where}: tensors on more than one device")
+    return dev
+
+
+def _home(where: str, stream, ws, *structs):
+    """(stream handle, device index) of a call whose workspace and structs have to be on the
+    current device, the one that the launch goes to."""
+    dev = ws.get_device()
+    if dev < 0:
         raise ResaError(4, f"{where}: the workspace is on {ws.device}")
+    for s in structs:
+        if s.device != dev and s.device is not None:
+            raise ResaError(4, f"{where}: {type(s).__name__} over memory of another device than the "
+                               "workspace's, or of the host")
     handle, device = _cuda()
-    if ws.device.index != device():
+    if dev != device():
         raise ResaError(4, f"{where}: the workspace is on {ws.device}, not the current device")
-    return handle(ws.device.index)
+    return (handle(dev) if stream is None else _stream(stream)), dev
+
+
+def _placed(where: str, cache: "resa_cache_t") -> "resa_cache_t":
+    """A cache of make_cache, whose device is looked up once, by the first call that asks."""
+    if cache.device is None and cache.tensors:
+        cache.device = _device(where, cache.tensors)
+    return cache
+
+
+def _at(where: str, name: str, t, dev: int) -> Optional[int]:
+    """_ptr of a tensor that has to be on device ``dev``."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev:
+        raise ResaError(4, f"{where}: {name} is on {t.device}, not on the workspace's device")
+    return t.data_ptr()
 
 
 def _check(st: int, where: str):
@@ -174,19 +213,25 @@ def _keep(struct, *tensors):
     return struct
 
 
+def _keep_at(where: str, struct, *tensors):
+    """_keep, of tensors that have to be on one device."""
+    struct.device = _device(where, tensors)
+    return _keep(struct, *tensors)
+
+
 def make_cache(k, v, desc, page_table, seq_len, rows=None) -> resa_cache_t:
     """Cache struct over torch tensors k/v [pages][Hkv][b][d] bf16, desc
     [pages][Hkv][2][d] bf16, page_table [B][max_pages] int32, seq_len [B] int32.
 
     With ``rows`` (int32 device tensor [n]) the call covers the n sequences in
     those rows of page_table / seq_len (the row map of resa_cache_t).  The struct
-    keeps page_table, seq_len and rows alive; the pages are the caller's to keep."""
+    keeps all of them alive."""
     nrows = int(page_table.shape[0])
     return _keep(resa_cache_t(_ptr(k), _ptr(v), _ptr(desc), _ptr(page_table), _ptr(seq_len),
                               nrows if rows is None else int(rows.numel()),
                               int(page_table.shape[1]), int(k.shape[0]), _ptr(rows),
                               0 if rows is None else nrows),
-                 page_table, seq_len, rows)
+                 k, v, desc, page_table, seq_len, rows)
 
 
 def _expect(name: str, t, dtype: str, shape=None):
@@ -218,7 +263,8 @@ def make_cache_q4(k, k_sf, v, v_sf, desc, page_table, seq_len, rows=None, k_scal
             ("k_scale", k_scale, "float32", (hkv,)), ("v_scale", v_scale, "float32", (hkv,))):
         _expect("make_cache_q4: " + name, t, dtype, shape)
     nrows = int(page_table.shape[0])
-    return _keep(resa_cache_q4_t(_ptr(k), _ptr(v), _ptr(k_sf), _ptr(v_sf), _ptr(desc),
+    return _keep_at("make_cache_q4", resa_cache_q4_t(
+                                 _ptr(k), _ptr(v), _ptr(k_sf), _ptr(v_sf), _ptr(desc),
                                  _ptr(page_table), _ptr(seq_len),
                                  nrows if rows is None else int(rows.numel()),
                                  int(page_table.shape[1]), int(k.shape[0]), _ptr(rows),
@@ -232,8 +278,9 @@ def make_rope(rot_dim: int, inv_freq, interleaved: bool = False,
     [rot_dim / 2] (None when rot_dim is 0)."""
     if rot_dim:
         _expect("make_rope: inv_freq", inv_freq, "float32", (rot_dim // 2,))
-    return _keep(resa_rope_t(rot_dim, 1 if interleaved else 0,
-                             _ptr(inv_freq) if rot_dim else None, mscale), inv_freq)
+    return _keep_at("make_rope", resa_rope_t(rot_dim, 1 if interleaved else 0,
+                                             _ptr(inv_freq) if rot_dim else None, mscale),
+                    inv_freq if rot_dim else None)
 
 
 def _token_stride(t, name: str) -> int:
@@ -259,10 +306,11 @@ def make_tokens(q, k, v, n_new=None, positions=None) -> resa_tokens_t:
         raise ResaError(2, "make_tokens: v has not k's heads, or the heads differ in size")
     _expect("make_tokens: n_new", n_new, "int32", (b,))
     _expect("make_tokens: positions", positions, "int32", (b, f))
-    return _keep(resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),
-                               0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"),
-                               _token_stride(v, "v"), int(k.shape[1]), _ptr(n_new),
-                               _ptr(positions)), q, k, v, n_new, positions)
+    return _keep_at("make_tokens",
+                    resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),
+                                  0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"),
+                                  _token_stride(v, "v"), int(k.shape[1]), _ptr(n_new),
+                                  _ptr(positions)), q, k, v, n_new, positions)
 
 
 # ---------------------------------------------------------------------------
@@ -354,43 +402,52 @@ def resa_sparse_decode_noalloc(cfg, cache, q, block_idx, block_cnt, max_topk: in
 
 def resa_append_rope(cfg, cache, rope, tokens, q_out, ws, stream=None):
     """Append fresh tokens to the bf16 cache, queries and keys rotated on the way."""
+    where = "resa_append_rope"
+    st, dev = _home(where, stream, ws, _placed(where, cache), rope, tokens)
     _check(lib().resa_append_rope(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
-                                  ctypes.byref(tokens), _ptr(q_out), _ptr(ws), ws.numel(),
-                                  _stream_at(stream, ws, "resa_append_rope")),
-           "resa_append_rope")
+                                  ctypes.byref(tokens), _at(where, "q_out", q_out, dev),
+                                  ws.data_ptr(), ws.numel(), st), where)
 
 
 def resa_append_rope_q4(cfg, cache, rope, tokens, q_out, ws, stream=None):
     """resa_append_rope into a 4-bit cache (make_cache_q4)."""
+    where = "resa_append_rope_q4"
+    st, dev = _home(where, stream, ws, cache, rope, tokens)
     _check(lib().resa_append_rope_q4(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
-                                     ctypes.byref(tokens), _ptr(q_out), _ptr(ws), ws.numel(),
-                                     _stream_at(stream, ws, "resa_append_rope_q4")),
-           "resa_append_rope_q4")
+                                     ctypes.byref(tokens), _at(where, "q_out", q_out, dev),
+                                     ws.data_ptr(), ws.numel(), st), where)
 
 
 def resa_expand_q4(cfg, cache, k_out, v_out, ws, stream=None):
     """Write a 4-bit cache's valid positions into bf16 pages k_out / v_out."""
-    _check(lib().resa_expand_q4(ctypes.byref(cfg), ctypes.byref(cache), _ptr(k_out), _ptr(v_out),
-                                _ptr(ws), ws.numel(), _stream_at(stream, ws, "resa_expand_q4")),
-           "resa_expand_q4")
+    where = "resa_expand_q4"
+    st, dev = _home(where, stream, ws, cache)
+    _check(lib().resa_expand_q4(ctypes.byref(cfg), ctypes.byref(cache),
+                                _at(where, "k_out", k_out, dev), _at(where, "v_out", v_out, dev),
+                                ws.data_ptr(), ws.numel(), st), where)
 
 
 def resa_sparse_decode_q4(cfg, cache, q, block_idx, block_cnt, max_topk: int, out, lse, ws,
                           stream=None):
     """resa_sparse_decode over a 4-bit cache."""
-    _check(lib().resa_sparse_decode_q4(ctypes.byref(cfg), ctypes.byref(cache), _ptr(q),
-                                       _ptr(block_idx), _ptr(block_cnt), max_topk, _ptr(out),
-                                       _ptr(lse), _ptr(ws), ws.numel(),
-                                       _stream_at(stream, ws, "resa_sparse_decode_q4")),
-           "resa_sparse_decode_q4")
+    where = "resa_sparse_decode_q4"
+    st, dev = _home(where, stream, ws, cache)
+    _check(lib().resa_sparse_decode_q4(ctypes.byref(cfg), ctypes.byref(cache),
+                                       _at(where, "q", q, dev),
+                                       _at(where, "block_idx", block_idx, dev),
+                                       _at(where, "block_cnt", block_cnt, dev), max_topk,
+                                       _at(where, "out", out, dev), _at(where, "lse", lse, dev),
+                                       ws.data_ptr(), ws.numel(), st), where)
 
 
 def resa_attention_q4(cfg, cache, f: int, n_new, q, out, lse, ws, stream=None):
     """Causal attention of each sequence's last n_new (None: f) tokens over its 4-bit cache."""
-    _check(lib().resa_attention_q4(ctypes.byref(cfg), ctypes.byref(cache), f, _ptr(n_new),
-                                   _ptr(q), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                   _stream_at(stream, ws, "resa_attention_q4")),
-           "resa_attention_q4")
+    where = "resa_attention_q4"
+    st, dev = _home(where, stream, ws, cache)
+    _check(lib().resa_attention_q4(ctypes.byref(cfg), ctypes.byref(cache), f,
+                                   _at(where, "n_new", n_new, dev), _at(where, "q", q, dev),
+                                   _at(where, "out", out, dev), _at(where, "lse", lse, dev),
+                                   ws.data_ptr(), ws.numel(), st), where)
 
 
 def resa_kernels_per_call(entry_point: str) -> int:

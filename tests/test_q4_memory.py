@@ -45,3 +45,141 @@ def test_tokens_of_unlike_heads_are_refused():
         with pytest.raises(R.ResaError) as e:
             R.make_tokens(q, k, v)
         assert e.value.status == 2
+
+
+class FakeWorkspace:
+    """The workspace of a device that this machine need not have."""
+
+    def __init__(self, index=0):
+        self.index, self.device = index, f"cuda:{index}"
+
+    def get_device(self):
+        return self.index
+
+    def numel(self):
+        return 1 << 34
+
+    def data_ptr(self):
+        return 0x10000000
+
+
+class Elsewhere:
+    """A tensor whose memory is on the given device."""
+
+    def __init__(self, t, index):
+        self.t, self.index = t, index
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+CFG = R.make_config(8, 2, 64, 16)
+
+
+def calls(index=0):
+    """Each entry point's call with every tensor on device `index`: name -> (function of the
+    replaced arguments, the arguments)."""
+    put = lambda t: Elsewhere(t, index)
+    table = put(torch.zeros(2, 3, dtype=torch.int32))
+    e = LayerCacheQ4.empty(6, 2, 16, 64, torch.zeros(2, 3, dtype=torch.int32))
+    c4 = [put(x) for x in (e.k, e.k_sf, e.v, e.v_sf, e.desc)] + [table, put(e.seq_len)]
+    k16 = put(torch.zeros(6, 2, 16, 64, dtype=torch.bfloat16))
+    f = 5
+    x = lambda *s, dtype=torch.bfloat16: put(torch.zeros(*s, dtype=dtype))
+    i32, f32 = torch.int32, torch.float32
+    inv, tok = x(32, dtype=f32), (x(2, f, 8, 64), x(2, f, 2, 64), x(2, f, 2, 64))
+
+    def append(four, c=None, inv=inv, q=tok[0], k=tok[1], v=tok[2], n=None, q_out=x(2, f, 8, 64),
+               ws=FakeWorkspace(index), cfg=CFG, stream=None):
+        cache = R.make_cache_q4(*(c or c4)) if four else \
+            R.make_cache(*(c or (k16, k16, c4[4], table, c4[6])))
+        (R.resa_append_rope_q4 if four else R.resa_append_rope)(
+            cfg, cache, R.make_rope(64, inv), R.make_tokens(q, k, v, n_new=n), q_out, ws, stream)
+
+    def expand(c=None, k_out=k16, v_out=k16, ws=FakeWorkspace(index), cfg=CFG, stream=None):
+        R.resa_expand_q4(cfg, R.make_cache_q4(*(c or c4)), k_out, v_out, ws, stream)
+
+    def sparse(c=None, q=x(2, 8, 64), idx=x(2, 2, 4, dtype=i32), cnt=x(2, 2, dtype=i32), top=3,
+               out=x(2, 8, 64, dtype=f32), lse=x(2, 8, dtype=f32), ws=FakeWorkspace(index), cfg=CFG,
+               stream=None):
+        R.resa_sparse_decode_q4(cfg, R.make_cache_q4(*(c or c4)), q, idx, cnt, top, out, lse, ws, stream)
+
+    def attention(c=None, n=x(2, dtype=i32), q=x(2, f, 8, 64), out=x(2, f, 8, 64, dtype=f32),
+                  lse=x(2, f, 8, dtype=f32), ws=FakeWorkspace(index), cfg=CFG, stream=None):
+        R.resa_attention_q4(cfg, R.make_cache_q4(*(c or c4)), f, n, q, out, lse, ws, stream)
+
+    return c4, {"append": lambda **kw: append(False, **kw), "append4": lambda **kw: append(True, **kw),
+                "expand": expand, "sparse": sparse, "attention": attention}
+
+
+class Launches:
+    """Stands for the library: counts the calls that reach it."""
+
+    def __init__(self):
+        self.n = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.n += 1
+            return 0
+        return call
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """No library and no GPU: device 0 is the current one."""
+    x = Launches()
+    monkeypatch.setattr(R, "lib", lambda: x)
+    monkeypatch.setattr(R, "_cuda", lambda: ((lambda i: 0x77), (lambda: 0)))
+    return x
+
+
+def refused(f, launches, status, **kw):
+    n = launches.n
+    with pytest.raises(R.ResaError) as e:
+        f(**kw)
+    assert e.value.status == status and launches.n == n, kw
+
+
+def test_memory_of_the_host_or_of_another_device_is_refused(launches):
+    c4, run = calls(0)
+    for f in run.values():
+        f()
+        f(stream=0)
+    assert launches.n == 10
+    far = lambda t: [Elsewhere(t, -1), Elsewhere(t, 1)]
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype)
+    i32, f32 = torch.int32, torch.float32
+    for name in ("append", "append4"):
+        for kw in ([dict(inv=t) for t in far(z(32, dtype=f32))] + [dict(q_out=t) for t in far(z(2, 5, 8, 64))]
+                   + [dict(n=t) for t in far(z(2, dtype=i32))] + [dict(k=t) for t in far(z(2, 5, 2, 64))]):
+            refused(run[name], launches, 4, **kw)
+    for name in ("append4", "expand", "sparse", "attention"):
+        for i, t in enumerate(c4):
+            for there in far(t.t):
+                refused(run[name], launches, 4, c=c4[:i] + [there] + c4[i + 1:])
+        all_there = [[Elsewhere(t.t, d) for t in c4] for d in (-1, 1)]
+        for c in all_there:
+            refused(run[name], launches, 4, c=c)
+    for t in far(z(6, 2, 16, 64)):
+        refused(run["expand"], launches, 4, k_out=t)
+        refused(run["expand"], launches, 4, v_out=t)
+        refused(run["append"], launches, 4, c=(t, t, c4[4], c4[5], c4[6]))
+        refused(run["append"], launches, 4, c=(Elsewhere(t.t, 0), t, c4[4], c4[5], c4[6]))
+    for kw in (dict(q=z(2, 8, 64)), dict(idx=z(2, 2, 4, dtype=i32)), dict(cnt=z(2, 2, dtype=i32)),
+               dict(out=z(2, 8, 64, dtype=f32)), dict(lse=z(2, 8, dtype=f32))):
+        refused(run["sparse"], launches, 4, **kw)
+    for kw in (dict(q=z(2, 5, 8, 64)), dict(n=z(2, dtype=i32)), dict(out=z(2, 5, 8, 64, dtype=f32)),
+               dict(lse=z(2, 5, 8, dtype=f32))):
+        refused(run["attention"], launches, 4, **kw)
+
+
+def test_calls_away_from_the_current_device_are_refused(launches):
+    """Everything on device 1 while device 0 is current, with a stream given or not."""
+    _, run = calls(1)
+    for f in run.values():
+        refused(f, launches, 4)
+        refused(f, launches, 4, stream=0x1234)
