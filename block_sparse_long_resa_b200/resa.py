@@ -44,7 +44,8 @@ class resa_cache_t(ctypes.Structure):
                 ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("rows", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int32)]
-    device, tensors = None, ()  # as make_cache sets them: index of the tensors' device
+    # as make_cache sets them: index of the tensors' device, (kv heads, block, head) of the pages
+    device, dims, tensors = None, None, ()
 
 
 class resa_cache_q4_t(ctypes.Structure):
@@ -55,7 +56,7 @@ class resa_cache_q4_t(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("rows", ctypes.c_void_p),
                 ("table_rows", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p)]
-    device = None  # index of the tensors' device; None: made of addresses
+    device = dims = None  # of the tensors it was made of; None: of addresses
 
 
 class resa_rope_t(ctypes.Structure):
@@ -69,7 +70,7 @@ class resa_tokens_t(ctypes.Structure):
                 ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
                 ("v_stride", ctypes.c_int64), ("f", ctypes.c_int32),
                 ("n_new", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
-    device = None
+    device = dims = None  # dims: (batch, q heads or None, kv heads, head)
 
 
 _lib = None
@@ -120,6 +121,9 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_addr = ctypes.addressof
+
+
 def _ptr(t) -> Optional[int]:
     if t is None:
         return None
@@ -161,36 +165,66 @@ def _device(where: str, tensors) -> Optional[int]:
     return dev
 
 
-def _home(where: str, stream, ws, *structs):
-    """(stream handle, device index) of a call whose workspace and structs have to be on the
-    current device, the one that the launch goes to."""
+def _home(where: str, stream, ws, cfg, cache):
+    """(stream handle, device index) of a call whose workspace and cache have to be on the
+    current device, the one that the launch goes to, and whose cache has to be of the
+    configuration's shape."""
     dev = ws.get_device()
     if dev < 0:
         raise ResaError(4, f"{where}: the workspace is on {ws.device}")
-    for s in structs:
-        if s.device != dev and s.device is not None:
-            raise ResaError(4, f"{where}: {type(s).__name__} over memory of another device than the "
-                               "workspace's, or of the host")
+    if cache.dims is not None:
+        if cache.device != dev:
+            raise ResaError(4, f"{where}: the cache is not on the workspace's device")
+        if cache.dims != (cfg.num_kv_heads, cfg.block_size, cfg.head_dim):
+            raise ResaError(2, f"{where}: (kv heads, block, head) are {cache.dims} in the cache, not "
+                               f"{(cfg.num_kv_heads, cfg.block_size, cfg.head_dim)}")
     handle, device = _cuda()
     if dev != device():
         raise ResaError(4, f"{where}: the workspace is on {ws.device}, not the current device")
     return (handle(dev) if stream is None else _stream(stream)), dev
 
 
-def _placed(where: str, cache: "resa_cache_t") -> "resa_cache_t":
-    """A cache of make_cache, whose device is looked up once, by the first call that asks."""
-    if cache.device is None and cache.tensors:
-        cache.device = _device(where, cache.tensors)
-    return cache
+def _look_over(where: str, cfg, cache):
+    """Check the memory of a cache of make_cache, which checks nothing, at the first call that
+    asks.  (A struct of addresses is the caller's to vouch for.)"""
+    if not cache.tensors:
+        return
+    k, v, desc, page_table, seq_len, rows = cache.tensors
+    dims = tuple(k.shape[1:]) if k.dim() == 4 else (cfg.num_kv_heads, cfg.block_size, cfg.head_dim)
+    n = k.shape[0] * dims[0] * dims[1] * dims[2]
+    device = _device(where, cache.tensors)
+    for name, t, dtype, size in (
+            ("k", k, "bfloat16", n), ("v", v, "bfloat16", n), ("desc", desc, "bfloat16", 2 * n // dims[1]),
+            ("page_table", page_table, "int32", 0), ("seq_len", seq_len, "int32", page_table.shape[0]),
+            ("rows", rows, "int32", 0)):
+        if t is None or isinstance(t, int):
+            continue
+        _expect(f"{where}: {name}", t, dtype)
+        if t.numel() < size:
+            raise ResaError(2, f"{where}: {name} has {t.numel()} elements of {size}")
+    cache.device, cache.dims = device, dims
 
 
-def _at(where: str, name: str, t, dev: int) -> Optional[int]:
-    """_ptr of a tensor that has to be on device ``dev``."""
+@functools.lru_cache(maxsize=None)
+def _dtypes():
+    import torch
+    return torch.bfloat16, torch.float32, torch.int32
+
+
+def _at(where: str, name: str, t, dtype, size: int, dev: int) -> Optional[int]:
+    """_ptr of a tensor that has to hold `size` bytes of dtype, one element behind the other, on
+    device ``dev``.  (It may be larger, and of any shape.)"""
     if t is None or isinstance(t, int):
         return t
+    if (t.dtype is dtype and t.nbytes >= size and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ResaError(4, f"{where}: {name} is on {t.device}, not on the workspace's device")
-    return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ResaError(4, f"{where}: {name} is {t.dtype}, not {dtype}")
+    if t.nbytes < size:
+        raise ResaError(2, f"{where}: {name} has {t.nbytes} bytes of {size}")
+    raise ResaError(4, f"{where}: {name} is not contiguous")
 
 
 def _check(st: int, where: str):
@@ -263,13 +297,15 @@ def make_cache_q4(k, k_sf, v, v_sf, desc, page_table, seq_len, rows=None, k_scal
             ("k_scale", k_scale, "float32", (hkv,)), ("v_scale", v_scale, "float32", (hkv,))):
         _expect("make_cache_q4: " + name, t, dtype, shape)
     nrows = int(page_table.shape[0])
-    return _keep_at("make_cache_q4", resa_cache_q4_t(
-                                 _ptr(k), _ptr(v), _ptr(k_sf), _ptr(v_sf), _ptr(desc),
+    c = _keep_at("make_cache_q4",
+                 resa_cache_q4_t(_ptr(k), _ptr(v), _ptr(k_sf), _ptr(v_sf), _ptr(desc),
                                  _ptr(page_table), _ptr(seq_len),
                                  nrows if rows is None else int(rows.numel()),
                                  int(page_table.shape[1]), int(k.shape[0]), _ptr(rows),
                                  0 if rows is None else nrows, _ptr(k_scale), _ptr(v_scale)),
                  k, k_sf, v, v_sf, desc, page_table, seq_len, rows, k_scale, v_scale)
+    c.dims = (hkv, b, 2 * half)
+    return c
 
 
 def make_rope(rot_dim: int, inv_freq, interleaved: bool = False,
@@ -306,11 +342,13 @@ def make_tokens(q, k, v, n_new=None, positions=None) -> resa_tokens_t:
         raise ResaError(2, "make_tokens: v has not k's heads, or the heads differ in size")
     _expect("make_tokens: n_new", n_new, "int32", (b,))
     _expect("make_tokens: positions", positions, "int32", (b, f))
-    return _keep_at("make_tokens",
-                    resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),
-                                  0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"),
-                                  _token_stride(v, "v"), int(k.shape[1]), _ptr(n_new),
-                                  _ptr(positions)), q, k, v, n_new, positions)
+    x = _keep_at("make_tokens",
+                 resa_tokens_t(_ptr(q), _ptr(k), _ptr(v),
+                               0 if q is None else _token_stride(q, "q"), _token_stride(k, "k"),
+                               _token_stride(v, "v"), int(k.shape[1]), _ptr(n_new),
+                               _ptr(positions)), q, k, v, n_new, positions)
+    x.dims = (b, None if q is None else q.shape[2], k.shape[2], k.shape[3])
+    return x
 
 
 # ---------------------------------------------------------------------------
@@ -400,54 +438,103 @@ def resa_sparse_decode_noalloc(cfg, cache, q, block_idx, block_cnt, max_topk: in
            "resa_sparse_decode_noalloc")
 
 
+def _append_args(where: str, stream, cfg, cache, rope, tokens, q_out, ws):
+    """(stream handle, address of q_out) of a rotary append."""
+    st, dev = _home(where, stream, ws, cfg, cache)
+    hq, batch = cfg.num_q_heads, cache.batch
+    if rope.device is not None and rope.device != dev:
+        raise ResaError(4, f"{where}: inv_freq is not on the workspace's device")
+    if tokens.dims is not None:
+        if tokens.device != dev:
+            raise ResaError(4, f"{where}: the tokens are not on the workspace's device")
+        dims = (batch, None if tokens.dims[1] is None else hq, cfg.num_kv_heads, cfg.head_dim)
+        if tokens.dims != dims:
+            raise ResaError(2, f"{where}: (batch, q heads, kv heads, head) are {tokens.dims} in the "
+                               f"tokens, {dims} in the call")
+    return st, _at(where, "q_out", q_out, _dtypes()[0], 2 * batch * tokens.f * hq * cfg.head_dim, dev)
+
+
 def resa_append_rope(cfg, cache, rope, tokens, q_out, ws, stream=None):
     """Append fresh tokens to the bf16 cache, queries and keys rotated on the way."""
-    where = "resa_append_rope"
-    st, dev = _home(where, stream, ws, _placed(where, cache), rope, tokens)
-    _check(lib().resa_append_rope(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
-                                  ctypes.byref(tokens), _at(where, "q_out", q_out, dev),
-                                  ws.data_ptr(), ws.numel(), st), where)
+    if cache.dims is None:
+        _look_over("resa_append_rope", cfg, cache)
+    st, out = _append_args("resa_append_rope", stream, cfg, cache, rope, tokens, q_out, ws)
+    st = lib().resa_append_rope(_addr(cfg), _addr(cache), _addr(rope), _addr(tokens), out,
+                                ws.data_ptr(), ws.nbytes, st)
+    if st != RESA_OK:
+        raise ResaError(st, "resa_append_rope")
 
 
 def resa_append_rope_q4(cfg, cache, rope, tokens, q_out, ws, stream=None):
     """resa_append_rope into a 4-bit cache (make_cache_q4)."""
-    where = "resa_append_rope_q4"
-    st, dev = _home(where, stream, ws, cache, rope, tokens)
-    _check(lib().resa_append_rope_q4(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(rope),
-                                     ctypes.byref(tokens), _at(where, "q_out", q_out, dev),
-                                     ws.data_ptr(), ws.numel(), st), where)
+    st, out = _append_args("resa_append_rope_q4", stream, cfg, cache, rope, tokens, q_out, ws)
+    st = lib().resa_append_rope_q4(_addr(cfg), _addr(cache), _addr(rope), _addr(tokens), out,
+                                   ws.data_ptr(), ws.nbytes, st)
+    if st != RESA_OK:
+        raise ResaError(st, "resa_append_rope_q4")
 
 
 def resa_expand_q4(cfg, cache, k_out, v_out, ws, stream=None):
     """Write a 4-bit cache's valid positions into bf16 pages k_out / v_out."""
     where = "resa_expand_q4"
-    st, dev = _home(where, stream, ws, cache)
-    _check(lib().resa_expand_q4(ctypes.byref(cfg), ctypes.byref(cache),
-                                _at(where, "k_out", k_out, dev), _at(where, "v_out", v_out, dev),
-                                ws.data_ptr(), ws.numel(), st), where)
+    st, dev = _home(where, stream, ws, cfg, cache)
+    bf16, _, _ = _dtypes()
+    n = 2 * cache.num_pages * cfg.num_kv_heads * cfg.block_size * cfg.head_dim
+    st = lib().resa_expand_q4(_addr(cfg), _addr(cache), _at(where, "k_out", k_out, bf16, n, dev),
+                              _at(where, "v_out", v_out, bf16, n, dev), ws.data_ptr(), ws.nbytes, st)
+    if st != RESA_OK:
+        raise ResaError(st, where)
 
 
 def resa_sparse_decode_q4(cfg, cache, q, block_idx, block_cnt, max_topk: int, out, lse, ws,
                           stream=None):
     """resa_sparse_decode over a 4-bit cache."""
     where = "resa_sparse_decode_q4"
-    st, dev = _home(where, stream, ws, cache)
-    _check(lib().resa_sparse_decode_q4(ctypes.byref(cfg), ctypes.byref(cache),
-                                       _at(where, "q", q, dev),
-                                       _at(where, "block_idx", block_idx, dev),
-                                       _at(where, "block_cnt", block_cnt, dev), max_topk,
-                                       _at(where, "out", out, dev), _at(where, "lse", lse, dev),
-                                       ws.data_ptr(), ws.numel(), st), where)
+    st, dev = _home(where, stream, ws, cfg, cache)
+    bf16, f32, i32 = _dtypes()
+    batch = cache.batch
+    rows, units = 4 * batch * cfg.num_q_heads, 4 * batch * cfg.num_kv_heads  # bytes of a word each
+    n = rows * cfg.head_dim
+    try:  # the checks of _at, in line: seven calls of it take 1 us
+        fit = (q.dtype is bf16 and q.nbytes >= n // 2 and q.get_device() == dev and q.is_contiguous()
+               and block_idx.dtype is i32 and block_idx.nbytes >= units * (max_topk + 1)
+               and block_idx.get_device() == dev and block_idx.is_contiguous()
+               and block_cnt.dtype is i32 and block_cnt.nbytes >= units
+               and block_cnt.get_device() == dev and block_cnt.is_contiguous()
+               and out.dtype is f32 and out.nbytes >= n and out.get_device() == dev
+               and out.is_contiguous()
+               and (lse is None or (lse.dtype is f32 and lse.nbytes >= rows
+                                    and lse.get_device() == dev and lse.is_contiguous())))
+    except AttributeError:  # an address among them
+        fit = False
+    if fit:
+        p = (q.data_ptr(), block_idx.data_ptr(), block_cnt.data_ptr(), max_topk, out.data_ptr(),
+             None if lse is None else lse.data_ptr())
+    else:
+        p = (_at(where, "q", q, bf16, n // 2, dev),
+             _at(where, "block_idx", block_idx, i32, units * (max_topk + 1), dev),
+             _at(where, "block_cnt", block_cnt, i32, units, dev), max_topk,
+             _at(where, "out", out, f32, n, dev), _at(where, "lse", lse, f32, rows, dev))
+    st = lib().resa_sparse_decode_q4(_addr(cfg), _addr(cache), *p, ws.data_ptr(), ws.nbytes, st)
+    if st != RESA_OK:
+        raise ResaError(st, where)
 
 
 def resa_attention_q4(cfg, cache, f: int, n_new, q, out, lse, ws, stream=None):
     """Causal attention of each sequence's last n_new (None: f) tokens over its 4-bit cache."""
     where = "resa_attention_q4"
-    st, dev = _home(where, stream, ws, cache)
-    _check(lib().resa_attention_q4(ctypes.byref(cfg), ctypes.byref(cache), f,
-                                   _at(where, "n_new", n_new, dev), _at(where, "q", q, dev),
-                                   _at(where, "out", out, dev), _at(where, "lse", lse, dev),
-                                   ws.data_ptr(), ws.numel(), st), where)
+    st, dev = _home(where, stream, ws, cfg, cache)
+    bf16, f32, i32 = _dtypes()
+    batch = cache.batch
+    rows = 4 * batch * f * cfg.num_q_heads  # bytes of a word each
+    n = rows * cfg.head_dim
+    st = lib().resa_attention_q4(
+        _addr(cfg), _addr(cache), f,
+        n_new if n_new is None else _at(where, "n_new", n_new, i32, 4 * batch, dev),
+        _at(where, "q", q, bf16, n // 2, dev), _at(where, "out", out, f32, n, dev),
+        lse if lse is None else _at(where, "lse", lse, f32, rows, dev), ws.data_ptr(), ws.nbytes, st)
+    if st != RESA_OK:
+        raise ResaError(st, where)
 
 
 def resa_kernels_per_call(entry_point: str) -> int:

@@ -51,13 +51,10 @@ class FakeWorkspace:
     """The workspace of a device that this machine need not have."""
 
     def __init__(self, index=0):
-        self.index, self.device = index, f"cuda:{index}"
+        self.index, self.device, self.nbytes = index, f"cuda:{index}", 1 << 34
 
     def get_device(self):
         return self.index
-
-    def numel(self):
-        return 1 << 34
 
     def data_ptr(self):
         return 0x10000000
@@ -183,3 +180,58 @@ def test_calls_away_from_the_current_device_are_refused(launches):
     for f in run.values():
         refused(f, launches, 4)
         refused(f, launches, 4, stream=0x1234)
+
+
+def test_tensors_of_other_sizes_and_types_are_refused(launches):
+    c4, run = calls(0)
+    put = lambda t: Elsewhere(t, 0)
+    z = lambda *s, dtype=torch.bfloat16: put(torch.zeros(*s, dtype=dtype))
+    i32, f32 = torch.int32, torch.float32
+    # a configuration that is not the cache's
+    for cfg in (R.make_config(8, 4, 64, 16), R.make_config(8, 2, 128, 16), R.make_config(8, 2, 64, 32),
+                R.make_config(8, 1, 64, 16)):
+        for f in run.values():
+            refused(f, launches, 2, cfg=cfg)
+    for name in ("append", "append4"):
+        f = run[name]
+        # tokens of fewer sequences, of other heads
+        refused(f, launches, 2, q=z(1, 5, 8, 64), k=z(1, 5, 2, 64), v=z(1, 5, 2, 64))
+        refused(f, launches, 2, q=z(2, 5, 4, 64))
+        refused(f, launches, 2, q=z(2, 5, 0, 64))
+        refused(f, launches, 2, k=z(2, 5, 1, 64), v=z(2, 5, 1, 64))
+        refused(f, launches, 2, q=z(2, 5, 8, 32), k=z(2, 5, 2, 32), v=z(2, 5, 2, 32))
+        # a place for the queries that is too small, of other numbers, or with gaps
+        refused(f, launches, 2, q_out=z(2, 4, 8, 64))
+        refused(f, launches, 4, q_out=z(2, 5, 8, 64, dtype=f32))
+        refused(f, launches, 4, q_out=put(torch.zeros(2, 5, 8, 128, dtype=torch.bfloat16)[..., :64]))
+        f(q=None, q_out=None)
+        f(q_out=z(2 * 5 * 8 * 64 + 64))
+    k16, table, lens = z(6, 2, 16, 64), c4[5], c4[6]
+    for c in ((k16, z(5, 2, 16, 64), c4[4], table, lens), (k16, k16, z(6, 2, 1, 64), table, lens),
+              (k16, k16, c4[4], table, z(1, dtype=i32))):
+        refused(run["append"], launches, 2, c=c)
+    for c in ((z(6, 2, 16, 64, dtype=f32), k16, c4[4], table, lens),
+              (k16, k16, c4[4], table, z(2, dtype=torch.int64)),
+              (k16, k16, c4[4], z(2, 3, dtype=torch.int64), lens),
+              (k16, k16, c4[4], put(torch.zeros(2, 6, dtype=i32)[:, :3]), lens)):
+        refused(run["append"], launches, 4, c=c)
+    for name in ("k_out", "v_out"):
+        refused(run["expand"], launches, 2, **{name: z(5, 2, 16, 64)})
+        refused(run["expand"], launches, 4, **{name: z(6, 2, 16, 64, dtype=torch.float16)})
+    for status, kw in ((2, dict(q=z(1, 8, 64))), (4, dict(q=z(2, 8, 64, dtype=f32))),
+                       (4, dict(q=put(torch.zeros(2, 64, 8, dtype=torch.bfloat16).transpose(1, 2)))),
+                       (2, dict(top=4)), (2, dict(idx=z(2, 2, 3, dtype=i32))),
+                       (4, dict(idx=z(2, 2, 4, dtype=torch.int64))), (2, dict(cnt=z(2, dtype=i32))),
+                       (4, dict(cnt=z(2, 2, dtype=f32))), (4, dict(out=z(2, 8, 64))),
+                       (2, dict(out=z(2, 8, 32, dtype=f32))), (2, dict(lse=z(8, dtype=f32))),
+                       (4, dict(lse=z(2, 8)))):
+        refused(run["sparse"], launches, status, **kw)
+    run["sparse"](lse=None)
+    for status, kw in ((2, dict(q=z(2, 4, 8, 64))), (4, dict(q=z(2, 5, 8, 64, dtype=f32))),
+                       (2, dict(n=z(1, dtype=i32))), (4, dict(n=z(2, dtype=torch.int64))),
+                       (4, dict(out=z(2, 5, 8, 64))), (2, dict(out=z(2, 8, 64, dtype=f32))),
+                       (2, dict(lse=z(2, 8, dtype=f32))), (4, dict(lse=z(2, 5, 8)))):
+        refused(run["attention"], launches, status, **kw)
+    run["attention"](lse=None, n=None)
+    # buffers may be larger than the call
+    run["attention"](q=z(4, 5, 8, 64), out=z(4, 5, 8, 64, dtype=f32), lse=z(4, 5, 8, dtype=f32))
