@@ -174,7 +174,7 @@ __device__ __forceinline__ UnitInfo chunk_unit(const ChunkArgs &a, int u, uint32
         return x;
     }
     const int lim = x.L - x.n + (x.row0 + x.rows - 1) / a.g + 1;  // keys the last row sees
-    x.cnt = (lim + kKeys - 1) / kKeys;
+    x.cnt = ceil_div(lim, kKeys);
     return x;
 }
 
@@ -286,12 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int share = 0;
         if (per == 1 && units < grid && W > 0) {
             if (mine > 0) atomicMax(&sh_most, mine);
-            const int even = (W + grid - 1) / grid, last = (W + grid - units - 1) / (grid - units);
+            const int even = ceil_div(W, grid), last = ceil_div(W, grid - units);
 #pragma unroll 1
             for (int k = 0; k < 5; ++k) {  // the smallest of five shares that keep to the grid
                 share = max(kMinTiles, even + (int)((long long)(last - even) * k / 4));
                 int ctas;
-                const int mine_ctas = (mine + share - 1) / share, first = scan(mine_ctas, ctas);
+                const int mine_ctas = ceil_div(mine, share), first = scan(mine_ctas, ctas);
                 if (ctas > grid) continue;
                 if (min(share, sh_most) - max(kMinTiles, even) > kPieceTiles) share = 0;
                 if (share > 0 && first <= cta && cta < first + mine_ctas) {
@@ -299,12 +299,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sh_first = before;
                     sh_own = make_int2(mine_ctas, first);
                     sh_x[0] = before + (cta - first) * share;
-                    sh_x[1] = min(sh_x[0] + share, before + mine);
+                    sh_x[1] = sh_x[0] + min(share, before + mine - sh_x[0]);
                 }
                 break;
             }
         }
-        const int G = max(1, min(grid, (W + kMinTiles - 1) / kMinTiles));
+        const int G = max(1, min(grid, ceil_div(W, kMinTiles)));
         if (tid == 0) {
             sh_w = W;
             sh_ctas = G;
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_ok = lrow < p.rows;
             const int pos_first = p.L - p.n;
             const int lim = row_ok ? pos_first + rho / a.g + 1 : 0;  // keys the row sees
-            const int lim_warp = pos_first + (rho - lane) / a.g + 1;  // keys every row of the warp sees
+            const int lim_warp = pos_first + min((rho - lane) / a.g, p.n - 1) + 1;  // keys every row of the warp sees
             const size_t orow = ((size_t)p.b * a.f + rho / a.g) * hq + (size_t)p.h * a.g + rho % a.g;
             // The warp's 32 Q rows, each scaled to [2^8, 2^9) at its largest, into the swizzled
             // tile: D / 8 lanes a row, so that its loads are runs.
@@ -429,7 +429,7 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t tm = tile_mask[(tiles + i) & 3];
-                const bool full = tm == (1u << (kKeys / 16)) - 1u && t0 + kKeys <= lim_warp;
+                const bool full = tm == (1u << (kKeys / 16)) - 1u && t0 <= lim_warp - kKeys;
                 // the row's largest logit
                 float mt = -INFINITY, mt2 = -INFINITY;
                 if (full) {
@@ -668,7 +668,7 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
             bool ok = true;
             for (Walk w = start(); w.next(a, p);) {
                 const int T = p.t1 - p.t0;
-                const int nblk = (p.L + a.bs - 1) >> bs_shift;
+                const int nblk = ceil_div(p.L, a.bs);
                 const int32_t *pages = a.page_table + (size_t)p.row * a.max_pages;
                 // Page ids 32 blocks at a time, one a lane, the next window in flight.
                 const int blk0 = p.t0 * bpt, blk1 = min(nblk, p.t1 * bpt);

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
                 x.live = false;
                 return x;
             }
-            x.cnt = (x.L + a.bs - 1) / a.bs;
+            x.cnt = ceil_div(x.L, a.bs);
         } else {
             x.cnt = max(0, min(listed, a.max_topk + 1));
         }
@@ -283,18 +283,18 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             // Shares of `share` entries of one unit each, so that every CTA has one piece: the
             // smallest of five that keeps to the grid (the last one does), unless it is more
             // than kPieceKeys above the even share, which is what a second piece costs.
-            const int even = (W + grid - 1) / grid, last = (W + grid - units - 1) / (grid - units);
+            const int even = ceil_div(W, grid), last = ceil_div(W, grid - units);
 #pragma unroll 1
             for (int k = 0; k < 5; ++k) {
                 share = max(least, even + (int)((long long)(last - even) * k / 4));
                 int ctas;
-                const int first = scan((mine + share - 1) / share, ctas);
+                const int mine_ctas = ceil_div(mine, share), first = scan(mine_ctas, ctas);
                 if (ctas > grid) continue;
                 if ((long long)(min(share, sh_most) - max(least, even)) * a.bs > kPieceKeys) share = 0;
-                if (share > 0 && first <= cta && cta < first + (mine + share - 1) / share) {
+                if (share > 0 && first <= cta && cta < first + mine_ctas) {
                     sh_unit = tid;
                     sh_first = before;
-                    sh_own = make_int2((mine + share - 1) / share, first);
+                    sh_own = make_int2(mine_ctas, first);
                 }
                 if (share > 0 && cta >= ctas && tid == 0) sh_own = make_int2(0, 0);
                 break;
@@ -306,11 +306,11 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
             own_first = sh_own.y;
             if (own > 0) {
                 x0 = sh_first + (cta - own_first) * share;
-                x1 = min(x0 + share, sh_first + sh_units[sh_unit].x);
+                x1 = x0 + min(share, sh_first + sh_units[sh_unit].x - x0);
             }
         } else {
             // the line of entries in even shares
-            G = max(1, min(min(grid, W), max(units, (W + least - 1) / least)));
+            G = max(1, min(min(grid, W), max(units, ceil_div(W, least))));
             x0 = entry_of(cta);
             x1 = entry_of(cta + 1);
             if (x0 < x1 && before <= x0 && x0 < before + mine) {  // one thread: the unit entry x0 lies in
@@ -329,10 +329,10 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         }
     } else {
         const int cnt = unit_of(cta / a.cluster, false).cnt, rank = cta % a.cluster;
-        const int share = max(max(1, 32 * kWarps / a.bs), (cnt + a.cluster - 1) / a.cluster);
+        const int share = max(max(1, 32 * kWarps / a.bs), ceil_div(cnt, a.cluster));
         x0 = min(cnt, rank * share);
         x1 = min(cnt, x0 + share);
-        own = (cnt + share - 1) / share;
+        own = ceil_div(cnt, share);
         own_first = cta - rank;
     }
 
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * Q4Warps<D, NT>::kWarps, 1)
         const int b = un.b, h = un.h, L = un.L;
         const int rows_all = a.block_idx ? a.g : un.n * a.g;
         const int base_pos = a.block_idx ? 0 : L - un.n;  // row rho sees positions <= base_pos + rho / g
-        const int nblk_seq = (L + a.bs - 1) / a.bs;
+        const int nblk_seq = ceil_div(L, a.bs);
         const int32_t *list =
             a.block_idx ? a.block_idx + (size_t)u * (a.max_topk + 1) : nullptr;
         const int32_t *pages = a.page_table + (size_t)un.row * a.max_pages;

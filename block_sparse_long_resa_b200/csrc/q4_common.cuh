@@ -19,6 +19,11 @@ struct Q4Cache {
     const float *k_scale, *v_scale;
 };
 
+// ceil(a / b) of counts; a + b may pass 2^31.
+__device__ __forceinline__ int ceil_div(int a, int b) {
+    return (int)(((unsigned)a + (unsigned)b - 1u) / (unsigned)b);
+}
+
 __device__ __forceinline__ float head_scale(const float *g, int h) { return g ? g[h] : 1.f; }
 
 // Eight codes (channels c .. c+7, low nibble first) to four fp16 pairs.
