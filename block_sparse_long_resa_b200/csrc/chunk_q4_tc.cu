@@ -141,7 +141,8 @@ struct Piece {
     int row0, rows;   // first query row of the unit's group, rows of it
     int cnt, t0, t1;  // the unit's tiles, this piece's
     int ustart;       // the unit's first entry
-    int slot;         // partial slot of the CTA: 0 for its first piece
+    int u;            // its number
+    bool later;       // not the CTA's first piece
 };
 
 struct UnitInfo {
@@ -184,7 +185,8 @@ __device__ __forceinline__ int entry_of(int q, int W, int G) {
 }
 
 struct Walk {
-    int x, x1, ustart, u, slot;
+    int x, x1, ustart, u;
+    bool later;
     __device__ __forceinline__ bool next(const ChunkArgs &a, Piece &p) {
         while (x < x1) {
             const UnitInfo i = chunk_unit(a, u++, nullptr);
@@ -198,8 +200,9 @@ struct Walk {
                 p.rows = i.rows;
                 p.cnt = i.cnt;
                 p.ustart = ustart;
-                p.slot = slot;
-                slot = 1;
+                p.u = u - 1;
+                p.later = later;
+                later = true;
                 p.t0 = x - ustart;
                 ustart += i.cnt;
                 x = min(x1, ustart);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.x1 = sh_x[1];
         w.u = w.x < w.x1 ? sh_unit : 0;
         w.ustart = w.x < w.x1 ? sh_first : 0;
-        w.slot = 0;
+        w.later = false;
         return w;
     };
 
@@ -535,11 +538,11 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
             drain();
             const bool whole = p.t0 == 0 && p.t1 == p.cnt;
             const float inv = l > 0.f ? head_scale(a.c.v_scale, p.h) / l : (l == 0.f ? 0.f : l);
-            const size_t slot = (size_t)(2 * cta + p.slot) * kRows + lrow;
+            const size_t slot = p.later ? chunk_q4_later_slot(units, p.u, cta) : cta;
             // a partial lies as [32-row group][channel / 4][row in group][4], so that a warp's
             // stores are runs
             float4 *dst = whole ? reinterpret_cast<float4 *>(a.out + orow * D)
-                                : reinterpret_cast<float4 *>(a.part_o + (size_t)(2 * cta + p.slot) * kRows * D) +
+                                : reinterpret_cast<float4 *>(a.part_o + slot * kRows * D) +
                                       (size_t)(lrow / 32) * (D / 4) * 32 + lane;
             const int step = whole ? 1 : 32;
             if (row_ok) {
@@ -554,7 +557,7 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
             }
             if (row_ok) {
                 if (!whole)
-                    a.part_ml[slot] = make_float2(mx, l);
+                    a.part_ml[slot * kRows + lrow] = make_float2(mx, l);
                 else if (a.lse)
                     a.lse[orow] = l > 0.f ? (mx - kShift + log2f(l)) * 0.6931471805599453f
                                   : l == 0.f ? -INFINITY : l;
@@ -828,7 +831,8 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
         const int W = sh_w, G = sh_ctas, own = sh_own.x;
         const int q0 = own > 0 ? sh_own.y : (int)((((long long)p.ustart + 1) * G - 1) / W);
         const int q1 = own > 0 ? q0 + own - 1 : (int)((((long long)p.ustart + p.cnt) * G - 1) / W);
-        const int odd = own == 0 && entry_of(q0, W, G) < p.ustart ? 1 : 0;
+        const bool odd = own == 0 && entry_of(q0, W, G) < p.ustart;
+        const int slot0 = odd ? chunk_q4_later_slot(units, p.u, q0) : q0;
         // a warp 32 rows and four channels of them at a time, a lane a row
         const int k = q1 - q0 + 1, items = (p.rows + 31) / 32 * (D / 4);
         const int i0 = items * (cta - q0) / k, i1 = items * (cta - q0 + 1) / k;
@@ -841,7 +845,7 @@ uint4 xs[kLanes];  // all loads before the first use: one trip to memory
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
             for (int q = q0; q <= q1; ++q) {
-                const size_t sl = (size_t)(2 * q + (q == q0 ? odd : 0)) * kRows;
+                const size_t sl = (size_t)(q == q0 ? slot0 : q) * kRows;
                 const float2 ml = __ldcg(mls + sl);
                 const float4 v = __ldcg(os + sl * (D / 4));
                 const float mn = fmaxf(ms, ml.x);

@@ -174,18 +174,23 @@ resa_status_t resa_attention_q4(const resa_config_t *cfg, const resa_cache_q4_t 
     if (rect_row_groups(f, s.g) > kMaxRowTiles) return RESA_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(out) || !aligned4(n_new_opt) || !aligned4(lse_opt))
         return RESA_ERR_UNSUPPORTED;
-    const WsLayout w = layout_of(s, f * s.g <= kMaxGroup ? 0 : f);
+    WsLayout w = layout_of(s, 0);
+    const bool chunk = f * s.g > kMaxGroup;
+    const int units = (int)((long long)s.batch * s.hkv * rect_row_groups(f, s.g) < kNumSms
+                                ? s.batch * s.hkv * rect_row_groups(f, s.g) : kNumSms);
+    if (chunk) w.total = w.rect_o + chunk_q4_bytes(units, s.d);
     RESA_TRY(check_ws(ws, ws_bytes, w));
     if ((long long)s.batch * s.hkv * rect_row_groups(f, s.g) > 0x7fffffffLL / s.max_pages)
         return RESA_ERR_RANGE;  // entries of work are counted in 32 bits
     uint32_t *err = at<uint32_t>(ws, w.err);
-    if (f * s.g <= kMaxGroup)
+    if (!chunk)
         return cuda_status(launch_decode_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
                                             nullptr, nullptr, 0, sm_count(), at<float>(ws, w.dec_o),
                                             at<float>(ws, w.dec_lse), at<uint32_t>(ws, w.err + kDecBarrierOffset),
                                             out, lse_opt, err, stream));
     return cuda_status(launch_chunk_q4(s, c, cache->page_table, cache->seq_len, q, f, n_new_opt,
-                                       sm_count(), at<float>(ws, w.rect_o), at<float>(ws, w.rect_lse),
+                                       sm_count(), at<float>(ws, w.rect_o),
+                                       at<float>(ws, w.rect_o) + chunk_q4_partial_floats(units, s.d),
                                        at<uint32_t>(ws, w.rect_ticket), out, lse_opt, err, stream));
 }
 

@@ -157,8 +157,22 @@ cudaError_t launch_decode_q4(const Shape &s, const Q4Cache &c, const int32_t *pa
                              int max_topk, int sms, float *part_o, float *part_ml,
                              uint32_t *grid_bar, float *out, float *lse, uint32_t *err,
                              cudaStream_t st);
-// The same for chunks of more than kMaxGroup rows, on tcgen05 (part_o and part_ml: two row
-// groups a CTA; grid_bar: a 64-bit barrier word).
+// The chunk attention's partial row groups: one a CTA for the first unit of its share, and for a
+// unit that begins further on in a share one by its number (by the CTA's where there are more
+// units than CTAs).  A slot a unit and not a second one a CTA: with few units the partials are
+// then no larger than the bf16 rectification's, whose place in the workspace they take.
+__host__ __device__ inline int chunk_q4_later_slot(int units, int u, int cta) {
+    return kNumSms + (units < kNumSms ? u : cta);
+}
+inline size_t chunk_q4_slots(int units) { return kNumSms + (units < kNumSms ? units : kNumSms); }
+inline size_t chunk_q4_partial_floats(int units, int d) {  // of O; (max, sum) pairs follow
+    return chunk_q4_slots(units) * kRectRowsPerCta * d;
+}
+inline size_t chunk_q4_bytes(int units, int d) {
+    return (chunk_q4_partial_floats(units, d) + chunk_q4_slots(units) * kRectRowsPerCta * 2) * 4;
+}
+// The same for chunks of more than kMaxGroup rows, on tcgen05 (part_o and part_ml: chunk_q4_slots
+// row groups; grid_bar: a 64-bit barrier word).
 cudaError_t launch_chunk_q4(const Shape &s, const Q4Cache &c, const int32_t *page_table,
                             const int32_t *seq_len, const void *q, int f, const int32_t *n_new,
                             int sms, float *part_o, float *part_ml, uint32_t *grid_bar, float *out,

@@ -3,6 +3,7 @@
 #include <string.h>
 
 #include "api_common.cuh"
+#include "q4_common.cuh"
 
 namespace resa {
 namespace {
@@ -115,8 +116,13 @@ size_t resa_workspace_size(const resa_config_t *cfg, int32_t batch, int32_t max_
     size_t best = ws_layout(s.hq, s.hkv, s.d, s.bs, batch, max_pages, 0).total;
     for (int f = 1; f <= max_chunk; ++f) {
         if (rect_row_groups(f, s.g) > kMaxRowTiles) break;
-        const size_t t = ws_layout(s.hq, s.hkv, s.d, s.bs, batch, max_pages, f).total;
-        best = t > best ? t : best;
+        const WsLayout w = ws_layout(s.hq, s.hkv, s.d, s.bs, batch, max_pages, f);
+        best = w.total > best ? w.total : best;
+        if (f * s.g > kMaxGroup) {  // resa_attention_q4, whose partials lie in the same place
+            const long long units = (long long)batch * s.hkv * rect_row_groups(f, s.g);
+            const size_t t = w.rect_o + chunk_q4_bytes(units < kNumSms ? (int)units : kNumSms, s.d);
+            best = t > best ? t : best;
+        }
     }
     return best;
 }

@@ -135,10 +135,8 @@ struct WsLayout {
     size_t step_bars;    // u64 [B][Hkv][kStepBarWords] unit counter (zero between calls) and generation of the fused step
     size_t step_keys;    // u32 [B][Hkv][step_key_stride(max_pages)] block score keys of the fused step
     size_t step_part;    // u64 [kNumSms][kStepMaxGroup][d + 1] tagged per-CTA partials of the fused step
-    size_t rect_o;       // f32 [B][Hkv][row_groups][rect_splits][kRectRowsPerCta][d], or the 4-bit
-                         //   chunk attention's [2 kNumSms][kRectRowsPerCta][d]
-    size_t rect_lse;     // f32 [B][Hkv][row_groups][rect_splits][kRectRowsPerCta], or its float2
-                         //   (max, sum) [2 kNumSms][kRectRowsPerCta]
+    size_t rect_o;       // f32 [B][Hkv][row_groups][rect_splits][kRectRowsPerCta][d]
+    size_t rect_lse;     // f32 [B][Hkv][row_groups][rect_splits][kRectRowsPerCta]
     size_t total;
     int dec_splits;
     int row_tiles;   // rectification row groups of kRectRowsPerCta
@@ -176,11 +174,8 @@ inline WsLayout ws_layout(int hq, int hkv, int d, int bs, int batch, int max_pag
     w.step_keys = take(units * (size_t)step_key_stride(max_pages) * 4);
     w.step_part = take((size_t)kNumSms * kStepMaxGroup * (d + 1) * 8);
     size_t rect_rows = units * w.row_tiles * w.rect_splits * kRectRowsPerCta;
-    // the 4-bit chunk attention (more than kMaxGroup rows) keeps up to two partial row groups a CTA
-    const size_t q4_rows = chunk * g > kMaxGroup ? (size_t)2 * kNumSms * kRectRowsPerCta : 0;
-    const size_t o_rows = rect_rows > q4_rows ? rect_rows : q4_rows;
-    w.rect_o = take(o_rows * d * 4);
-    w.rect_lse = take(rect_rows * 4 > q4_rows * 8 ? rect_rows * 4 : q4_rows * 8);
+    w.rect_o = take(rect_rows * d * 4);
+    w.rect_lse = take(rect_rows * 4);
     w.total = off;
     return w;
 }
