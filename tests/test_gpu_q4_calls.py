@@ -8,7 +8,7 @@ from block_sparse_long_resa_b200 import resa as R
 from block_sparse_long_resa_b200.cache import workspace
 from oracle import q4
 from q4_problem import Problem, f64
-from test_gpu_q4 import check_rows
+from test_gpu_q4 import check_rows, ids
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,120 @@ def test_sequence_of_two_to_the_31_keys(cuda_device):
         got.append([x.clone() for x in (p.k4, p.v4, p.k_sf.view(torch.uint8), p.v_sf.view(torch.uint8), p.desc)])
     assert R.resa_check_device_status(ws, raise_on_error=False) == 0 and p.status() == 0
     assert all(torch.equal(x, y) for x, y in zip(*got)) and got[0][0].any()
+
+
+# --------------------------------------------------------------- long pieces of work, many units
+
+class Codes:
+    """A 4-bit cache of random codes and group scales over pages in random order, with logits spread
+    so far that a few keys take a row's weight: one tile read from a wrong page shows."""
+
+    def __init__(self, seed, lens, hq, hkv, d, b, dev, max_chunk=0, width=0):
+        self.rng = rng = np.random.default_rng(seed)
+        self.lens, self.hq, self.hkv, self.d, self.b, self.g, self.dev = lens, hq, hkv, d, b, hq // hkv, dev
+        need = [-(-L // b) for L in lens]
+        n, self.max_pages = sum(need), max(max(need), width // b)
+        order, at = rng.permutation(n).astype(np.int32), 0
+        self.table = np.full((len(lens), self.max_pages), n + 5, dtype=np.int32)
+        for i, m in enumerate(need):
+            self.table[i, :m] = order[at:at + m]
+            at += m
+        codes = lambda: rng.integers(0, 256, (n, hkv, b, d // 2), dtype=np.uint8)
+        scales = lambda lo, hi: rng.integers(lo, hi, (n, hkv, b, d // 16), dtype=np.uint8)
+        self.k, self.v, self.ks, self.vs = codes(), codes(), scales(0x28, 0x38), scales(0x20, 0x30)
+        up = lambda x: torch.from_numpy(x).to(dev)
+        self.cfg = R.make_config(hq, hkv, d, b)
+        self.c4 = R.make_cache_q4(up(self.k), up(self.ks), up(self.v), up(self.vs),
+                                  torch.zeros(n, hkv, 2, d, dtype=torch.bfloat16, device=dev), up(self.table),
+                                  torch.tensor(lens, dtype=torch.int32, device=dev))
+        self.ws = workspace(self.cfg, len(lens), self.max_pages, max_chunk, dev)
+
+    def queries(self, *shape):
+        return q4.bf16(self.rng.standard_normal((*shape, self.d)) * 3)
+
+    def keys_values(self, i, h, blocks=None):
+        L, b = self.lens[i], self.b
+        blocks = np.arange(-(-L // b)) if blocks is None else np.asarray(blocks)
+        pos = (blocks[:, None] * b + np.arange(b)).ravel()
+        pos = pos[pos < L]
+        page, slot = self.table[i, pos // b], pos % b
+        k = q4.values(q4.unpack(self.k[page, h, slot]), self.ks[page, h, slot])
+        return k, q4.values(q4.unpack(self.v[page, h, slot]), self.vs[page, h, slot]), pos
+
+    def attention(self, f, q, fresh=None):
+        n = len(self.lens)
+        out = torch.full((n, f, self.hq, self.d), 3.0, device=self.dev)
+        lse = torch.full((n, f, self.hq), 3.0, device=self.dev)
+        t_n = None if fresh is None else torch.tensor(fresh, dtype=torch.int32, device=self.dev)
+        R.resa_attention_q4(self.cfg, self.c4, f, t_n, torch.from_numpy(q).to(self.dev).bfloat16(), out, lse, self.ws)
+        assert R.resa_check_device_status(self.ws, raise_on_error=False) == 0
+        return f64(out), f64(lse)
+
+    def check(self, out, lse, q, i, h, n):
+        rows = lambda x: x[i, :n, h * self.g:(h + 1) * self.g].reshape((-1,) + x.shape[3:])
+        limit = np.repeat(np.arange(self.lens[i] - n, self.lens[i]) + 1, self.g)
+        check_rows(self, rows(out), rows(lse), rows(q), i, h, None, limit)
+
+
+@pytest.mark.parametrize("layout", [(16, 8, 128, 16), (128, 8, 64, 16), (24, 8, 64, 64)], ids=ids)
+def test_many_units_of_middling_length_whole(cuda_device, layout):
+    """Units for most SMs, each a CTA's: up to 22 steps a warp with 12 warps, 32 with 8, so that the
+    places of a piece's tiles are fetched anew on the way."""
+    hq, hkv, d, b = layout
+    lens = [8100 - 530 * i for i in range(15)] + [8191]
+    p = Codes(310, lens, hq, hkv, d, b, cuda_device, width=8192)
+    q = p.queries(16, 1, hq)
+    out, lse = p.attention(1, q)
+    for i in (0, 1, 7, 14, 15):
+        for h in (0, 3, 7):
+            p.check(out, lse, q, i, h, 1)
+
+
+@pytest.mark.parametrize("layout", [(32, 8, 64, 16), (128, 8, 64, 32)], ids=ids)
+def test_long_pieces_over_the_grid(cuda_device, layout):
+    """About 7000 keys a CTA (18 steps a warp with 12 warps, 27 with 8): every position, all blocks
+    listed in random order, and a chunk of 55 tiles a CTA."""
+    hq, hkv, d, b = layout
+    L = 130021
+    p = Codes(320, [L], hq, hkv, d, b, cuda_device, max_chunk=9)
+    q = p.queries(1, 9, hq)
+    for f in (1, 9):
+        qf = np.ascontiguousarray(q[:, :f])
+        out, lse = p.attention(f, qf)
+        for h in range(hkv):
+            p.check(out, lse, qf, 0, h, f)
+    nb = -(-L // b)
+    lists = np.stack([p.rng.permutation(nb) for _ in range(hkv)]).astype(np.int32)[None]
+    t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(cuda_device)
+    out = torch.zeros(1, hq, d, device=cuda_device)
+    lse = torch.zeros(1, hq, device=cuda_device)
+    R.resa_sparse_decode_q4(p.cfg, p.c4, t(q[:, 0]).bfloat16(), t(lists), torch.full((1, hkv), nb, dtype=torch.int32, device=cuda_device),
+                            nb - 1, out, lse, p.ws)
+    assert R.resa_check_device_status(p.ws, raise_on_error=False) == 0
+    for h in range(hkv):
+        r = slice(h * p.g, (h + 1) * p.g)
+        check_rows(p, f64(out)[0, r], f64(lse)[0, r], q[0, 0, r], 0, h, np.arange(nb), None)
+
+
+@pytest.mark.parametrize("layout,lens,f", [
+    ((32, 8, 128, 16), [1500 - 3 * i for i in range(16)], 6),          # pieces of 10 tiles, 16-token pages
+    ((16, 8, 64, 16), [20 + 7 * i for i in range(50)], 20),            # 400 units, one row group each
+    ((16, 8, 64, 32), [200 + 61 * i for i in range(30)], 200),         # 480 units of two row groups
+    ((4, 2, 128, 16), [9000, 130, 4000, 131, 132, 2500], 130),         # unequal: units that begin inside a share
+    ((14, 2, 64, 64), [300] * 60 + [9000], 40),
+], ids=lambda x: str(x) if isinstance(x, int) else "-".join(map(str, x[:4])))
+def test_chunks_of_long_pieces_and_many_units(cuda_device, layout, lens, f):
+    """The chunk kernel where a piece's pages take several fetches, where there are more units than
+    threads, and where shares begin and end inside units."""
+    hq, hkv, d, b = layout
+    p = Codes(330, lens, hq, hkv, d, b, cuda_device, max_chunk=f)
+    fresh = [min(f, L) - (i % 3 if L > f else 0) for i, L in enumerate(lens)]
+    fresh[1] = min(fresh[1], 3)
+    q = p.queries(len(lens), f, hq)
+    out, lse = p.attention(f, q, fresh)
+    for i in sorted({0, 1, 2, len(lens) // 2, len(lens) - 2, len(lens) - 1}):
+        assert (out[i, fresh[i]:] == 3.0).all() and (lse[i, fresh[i]:] == 3.0).all()
+        for h in sorted({0, hkv // 2, hkv - 1}):
+            p.check(out, lse, q, i, h, fresh[i])
+    o2, l2 = p.attention(f, q, fresh)
+    assert np.array_equal(out, o2) and np.array_equal(lse, l2)
