@@ -85,7 +85,7 @@ typedef enum {
 #define RESA_DEVERR_PAGE 0x2u      /* page_table entry outside [0, num_pages) */
 #define RESA_DEVERR_BLOCK 0x4u     /* block_idx entry outside the sequence */
 #define RESA_DEVERR_TOPK 0x8u      /* topk[b] > max_topk with more blocks available: clamped */
-#define RESA_DEVERR_CHUNK 0x10u    /* rectification chunk f > seq_len */
+#define RESA_DEVERR_CHUNK 0x10u    /* rectification chunk f > seq_len; n_new outside 0 .. f or above seq_len */
 #define RESA_DEVERR_TIMEOUT 0x20u  /* a bounded device wait gave up */
 #define RESA_DEVERR_ROW 0x40u      /* rows[i] outside [0, table_rows): sequence skipped */
 #define RESA_DEVERR_NONFINITE 0x80u /* NaN or infinity appended to a 4-bit cache: stored as a finite value */
@@ -129,7 +129,8 @@ typedef struct {
  * channel is stored as c = e2m1(y / s) (both to nearest even, saturating), which
  * stands for c * s * g.  c * s is exact in 16 bits.  Of a value that is not
  * finite, NaN is stored as 0 and infinity as the largest value (with
- * RESA_DEVERR_NONFINITE); group scales are finite.
+ * RESA_DEVERR_NONFINITE), and so is one whose y passes fp32's range; group scales
+ * are finite.
  *   k, v          [num_pages][Hkv][b][d / 2] bytes: channel 2j in the low and
  *                 2j+1 in the high four bits of byte j (e2m1: sign, 2 exponent
  *                 bits, 1 mantissa bit)
@@ -161,8 +162,9 @@ typedef struct {
  * head are rotated in pairs, the others are copied: with the token's position t
  * and a_i = t * inv_freq[i], pair i becomes
  *   (x1 cos a_i - x2 sin a_i, x2 cos a_i + x1 sin a_i) * mscale.
- * The angle is reduced in 64 bits, so far positions lose nothing; keys are
- * rotated in 64 bits and queries in 32, each rounded once to bf16. */
+ * The angle is worked out and reduced in 64 bits, so that far positions have as good
+ * angles as near ones; keys are rotated in 64 bits, rounded to fp32 and then to bf16,
+ * queries in 32 bits and rounded to bf16. */
 typedef struct {
     int32_t rot_dim;       /* 0 .. d, a multiple of 16; 0: no rotation */
     int32_t interleaved;   /* 0: pair i = channels (i, i + rot_dim/2); 1: (2i, 2i+1) */
@@ -186,8 +188,9 @@ typedef struct {
 } resa_tokens_t;
 
 /* Bytes of workspace needed for caches of `batch` sequences with up to
- * `max_pages` blocks each and rectification chunks of up to `max_chunk`
- * tokens (0 if resa_rectify_attention is not used). */
+ * `max_pages` blocks each and chunks of up to `max_chunk` tokens: the largest f
+ * of resa_rectify_attention, and of resa_attention_q4 where f * g > 16 (0 if
+ * there is neither).  The size covers every entry point. */
 RESA_API size_t resa_workspace_size(const resa_config_t *cfg, int32_t batch, int32_t max_pages,
                            int32_t max_chunk);
 
@@ -362,7 +365,7 @@ RESA_API resa_status_t resa_append_rope_q4(const resa_config_t *cfg, const resa_
 /* Expand a 4-bit cache into bf16 pages: k_out, v_out [num_pages][Hkv][b][d]
  * bf16 (the k, v of a resa_cache_t with the same page table, lengths and
  * descriptors).  Positions 0 .. seq_len-1 of the call's sequences are written
- * (values c * s * g rounded once to bf16), all others stay as they were.  A
+ * (values c * s * g rounded to fp32 and then to bf16), all others stay as they were.  A
  * sequence of length 0 is skipped.  At most 65535 sequences a call.  One launch. */
 RESA_API resa_status_t resa_expand_q4(const resa_config_t *cfg, const resa_cache_q4_t *cache,
                                       void *k_out, void *v_out, void *ws, size_t ws_bytes,
