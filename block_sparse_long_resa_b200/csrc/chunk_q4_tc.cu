@@ -74,11 +74,6 @@ struct ChunkSmem {
     static constexpr int kBytes = kRawOff + kRaw * kRawStage + 1024;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Two fp32 operations at a time.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -103,16 +98,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float pow2i(int k) { return __int_as_float((127 + k) << 23); }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-__device__ __forceinline__ void cp_async16_s(uint32_t smem_dst, const void *gsrc) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
-}
-
 // Registers a thread of this warpgroup has from here on (every warp of it runs this).
 template <int N, bool Up>
 __device__ __forceinline__ void set_regs() {
@@ -368,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (m < nm) {
                 constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
                 const int sub = lane / kLanes, c = lane % kLanes;
-uint4 xs[kLanes];  // all loads before the first use: one trip to memory
+                uint4 xs[kLanes];  // all loads before the first use: one trip to memory
 #pragma unroll
                 for (int it = 0; it < kLanes; ++it) {
                     const int qrow = m * 128 + (r - lane) + it * kRowsAt + sub, qrho = p.row0 + qrow;

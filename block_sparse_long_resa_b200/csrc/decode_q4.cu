@@ -47,7 +47,7 @@ namespace {
 
 template <int D, int NT>
 struct Q4Warps {
-    static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = NT == 1 ? 4 : 4;
+    static constexpr int kWarps = NT == 1 ? 12 : 8, kStages = 4;
 };
 // Units of at most so many keys are not split, by the width of the query tile, where a
 // cluster is no choice and where it is.  Measured (28 q / 4 kv heads, d 128, batch 16): 1024
@@ -85,15 +85,6 @@ struct Q4Smem {
     static constexpr int kRing = kWarps * kStages * kStage;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo) {
     hi = pack_f16(a, b);
     lo = pack_f16(a - f16_lo(hi), b - f16_hi(hi));
@@ -105,9 +96,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float pow2i(int k) {  // 2^k, k in [-126, 127]
-    return __int_as_float((127 + k) << 23);
 }
 
 // Byte offset of (token t, 8-byte piece p) of a V code tile: the 16-byte chunks
@@ -121,9 +109,6 @@ __device__ __forceinline__ uint32_t v_chunk(int t, int chunk) {
     return (uint32_t)(line * 128 + ((slot ^ ((line & 3) * 2)) << 4));
 }
 
-__device__ __forceinline__ void cp_async16_s(uint32_t smem_dst, const void *gsrc) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
-}
 // A load that stays where it is among the asynchronous copies.
 __device__ __forceinline__ uint4 ld_now(const uint4 *p) {
     uint4 x;

@@ -53,6 +53,10 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
     const uint32_t h = e4m3x2_to_f16(byte);
     return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -63,6 +67,18 @@ __device__ __forceinline__ float f16_lo(uint32_t p) {
 }
 __device__ __forceinline__ float f16_hi(uint32_t p) {
     return __half2float(__ushort_as_half((unsigned short)(p >> 16)));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int k) {  // 2^k, k in [-126, 127]
+    return __int_as_float((127 + k) << 23);
+}
+__device__ __forceinline__ void cp_async16_s(uint32_t smem_dst, const void *gsrc) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(gsrc) : "memory");
 }
 
 // Quantise one group of 16 bf16 values (pairs, channel 0 low) with 1/g = rg: codes
