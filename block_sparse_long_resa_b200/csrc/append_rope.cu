@@ -20,10 +20,11 @@
 // point: within 1/2 + 2^-17 of a step.)
 //
 // Measured (28 q / 4 kv heads, d 128): 8192 tokens, 152 MB, 32 us, 4.7 TB/s, bound by
-// the latency of 24 warps an SM (80 registers) more than by a unit (issue 55 %, exp and
-// sine unit 20 %, fp64 5 %); one token of each of 32 sequences 4.7 us, latency alone.
+// the latency of 24 warps an SM (80 registers) more than by a unit (issue 57 %, exp and
+// sine unit 22 %, fp64 5 %); one token of each of 32 sequences 5.2 us, the host's side of a
+// call.
 // Five ragged prompts of up to 2777 tokens into 4-bit pages (32 / 8 heads, d 128) and the
-// pages' expansion, 189 MB together, take 57 us: the groups' maxima, scales and codes
+// pages' expansion, 189 MB together, take 58 us: the groups' maxima, scales and codes
 // are added to each key and value.
 #include <cooperative_groups.h>
 
@@ -382,7 +383,7 @@ constexpr int kExpandAhead = 4;
 // Grid (ceil(max positions / kExpandTokens), batch, parts of their groups).  A thread turns a group of 16
 // channels (8 bytes of codes and a scale) into one 32-byte store, kAhead groups in
 // flight; a warp's reads and writes are contiguous runs.  Measured: 4 x 65536 tokens of 4
-// heads, d 128, 685 MB, 115 us, 6.0 TB/s (16-byte stores, one group in flight: 179 us).
+// heads, d 128, 685 MB, 114 us, 6.0 TB/s (16-byte stores, one group in flight: 179 us).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
     expand_q4_kernel(const __grid_constant__ Q4Cache c, const int32_t *__restrict__ page_table,

@@ -23,8 +23,9 @@
 // of a tile's first 64 keys runs while the softmax makes the others' weights.
 //
 // Precision.  q enters as fp16 scaled per row by a power of two (its 8 bits stay
-// exact), so Q K^T has exact products.  P enters as fp16 hi + lo (22 bits; fp16
-// alone would be 1.4e-4 off), both over the tile's S in tensor memory, 16 keys
+// exact down to 2^-25 of the row's largest channel), so Q K^T has exact products.  P
+// enters as fp16 hi + lo (22 bits, or 2^-36 of the row's largest weight where that is
+// coarser; fp16 alone would be 1.4e-4 off), both over the tile's S in tensor memory, 16 keys
 // (8 + 8 columns) at a time: P V takes twice the MMAs.  The matrix unit truncates
 // when it adds to its fp32 accumulator: 1.1e-5 off after 1024 additions.  So O
 // starts from zero every kChain tiles and is then added to its row in registers,
@@ -32,7 +33,8 @@
 // for 8, and 2 takes 1.2 % and 1.6 % longer than 4 and 8.
 //
 // Measured (28 q / 4 kv heads, d 128, 32 rows against 4 x 65536 tokens: 120 GFLOP,
-// 1.5 times that in MMAs, 153 MB): 185 us, 0.65 PFLOP/s, 0.97 PFLOP/s in MMAs.
+// 1.5 times that in MMAs, 153 MB): 204 us, 0.59 PFLOP/s, 0.88 PFLOP/s in MMAs (185 us on
+// boxes that hold a higher clock under this load).
 // Of a tile's 4900 cycles the chain of one M tile takes all: maximum 500, weights
 // 2600 (128 exponentials a thread at 4 a cycle and SM quarter are 1024), P V of the
 // second half 490, Q K^T 780.  An MMA with A in shared memory takes 97 cycles

@@ -25,16 +25,19 @@
 //      and r + 8; MMA k-step s uses its channels 4s .. 4s+3;
 //   V: lane (r, c) takes channels r * D/8 .. of tokens 2c, 2c+1, 2c+8, 2c+9, and
 //      pairs up the two tokens of a register with byte permutes.
-// c * s is exact in fp16.  q is scaled by a power of two per row into fp16's
-// range (its 8 bits stay exact), and P enters as fp16 hi + lo (22 bits) scaled
-// by 2^kShift, so the products lose nothing that fp32 accumulation keeps.  A step's
+// c * s is exact in fp16.  q is scaled by a power of two per row into fp16's range,
+// the row's largest channel to [2^8, 2^9): its 8 bits stay exact down to 2^-25 of the
+// largest, and a smaller channel is off by 2^-33 of that at most.  P enters as fp16
+// hi + lo scaled by 2^kShift: 22 bits, or 2^-36 of the row's largest weight where that is
+// coarser.  So the products lose nothing that fp32 accumulation keeps.  A step's
 // products start from zero and join the row in fp32 registers (see below).
 //
 // Measured (28 q / 4 kv heads, d 128): every position of one 262144-token sequence,
-// 151 MB, 51 us, 2.9 TB/s.  Instructions bound it: a warp's step of 32 tokens is
-// about 800 of them, issued at 2 a cycle and SM in 35 us; the rest is the first loads,
-// the barrier and the merge.  16 warps for 12 and two accumulator chains for one
-// changed nothing.  A list of 10 % of the same sequence's blocks, 15 MB: 16 us, nearly
+// 151 MB, 51 us, 2.9 TB/s.  Instructions bound it, by their latency more than by a unit:
+// a warp's step of 32 tokens is 722 of them, issued at 2.3 of 4 a cycle and SM in the
+// loop's 36 us (over the whole kernel, 26.6 M in 51 us, at 1.8); the rest is the share-out
+// and the first loads, 5.4 us, and the warps' merge, the barrier and the parts' merge, 8 us.
+// 16 warps for 12 and two accumulator chains for one changed nothing.  A list of 10 % of the same sequence's blocks, 15 MB: 16 us, nearly
 // all of it latency (list, page, tile, barrier, partials).
 #include <cooperative_groups.h>
 
@@ -53,7 +56,12 @@ struct Q4Warps {
 // cluster is no choice and where it is.  Measured (28 q / 4 kv heads, d 128, batch 16): 1024
 // keys 11.4 us whole, 11.4 by clusters of 2, 2048 keys 17 and 14 and, over the grid, 16-24;
 // batch 1: 512 keys 8.6 whole and 9.7 by clusters of 8, 1024 keys 11.0 and 10.1; with 16
-// heads a group 512 keys 11.1 and 11.5, 1024 keys 15 and 12.0.
+// heads a group 512 keys 11.1 and 11.5, 1024 keys 15 and 12.0.  These and the next constants
+// go by the width of the page table, which is all that the host knows, and were found with
+// tables as wide as the sequences.  In a table of 131072 keys the grid takes them all, for 2 to
+// 3 us more: one sequence of 2048 keys 11.1 us for 9.2, 8 of 1024 11.1 for 9.4, 16 of 2048
+// 15.4 for 12.5; d 64, where the same constants stand, 10.2 for 8.1, 10.3 for 8.3 and 13.0
+// for 10.1.
 constexpr int kWholeKeys[2] = {2048, 768}, kWholeNear[2] = {768, 512};
 // With units for most of the SMs: 128 units of 8192 keys 50 us whole and 54 split, 256 units of
 // 1 .. 2500 keys 30 and 57.
