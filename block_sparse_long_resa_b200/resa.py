@@ -447,10 +447,11 @@ def _append_args(where: str, stream, cfg, cache, rope, tokens, q_out, ws):
     if tokens.dims is not None:
         if tokens.device != dev:
             raise ResaError(4, f"{where}: the tokens are not on the workspace's device")
-        dims = (batch, None if tokens.dims[1] is None else hq, cfg.num_kv_heads, cfg.head_dim)
-        if tokens.dims != dims:
-            raise ResaError(2, f"{where}: (batch, q heads, kv heads, head) are {tokens.dims} in the "
-                               f"tokens, {dims} in the call")
+        n, heads, kv_heads, d = tokens.dims
+        if (n < batch or (heads is not None and heads != hq) or kv_heads != cfg.num_kv_heads
+                or d != cfg.head_dim):
+            raise ResaError(2, f"{where}: (batch, q heads, kv heads, head) are {tokens.dims} in the tokens, "
+                               f"{(batch, hq, cfg.num_kv_heads, cfg.head_dim)} in the call")
     return st, _at(where, "q_out", q_out, _dtypes()[0], 2 * batch * tokens.f * hq * cfg.head_dim, dev)
 
 

@@ -205,6 +205,7 @@ def test_tensors_of_other_sizes_and_types_are_refused(launches):
         refused(f, launches, 4, q_out=z(2, 5, 8, 64, dtype=f32))
         refused(f, launches, 4, q_out=put(torch.zeros(2, 5, 8, 128, dtype=torch.bfloat16)[..., :64]))
         f(q=None, q_out=None)
+        f(q=z(3, 5, 8, 64), k=z(3, 5, 2, 64), v=z(3, 5, 2, 64))    # of more sequences than the call's
         f(q_out=z(2 * 5 * 8 * 64 + 64))
     k16, table, lens = z(6, 2, 16, 64), c4[5], c4[6]
     for c in ((k16, z(5, 2, 16, 64), c4[4], table, lens), (k16, k16, z(6, 2, 1, 64), table, lens),
