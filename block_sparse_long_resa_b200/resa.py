@@ -509,14 +509,16 @@ def resa_sparse_decode_q4(cfg, cache, q, block_idx, block_cnt, max_topk: int, ou
     except AttributeError:  # an address among them
         fit = False
     if fit:
-        p = (q.data_ptr(), block_idx.data_ptr(), block_cnt.data_ptr(), max_topk, out.data_ptr(),
-             None if lse is None else lse.data_ptr())
+        st = lib().resa_sparse_decode_q4(
+            _addr(cfg), _addr(cache), q.data_ptr(), block_idx.data_ptr(), block_cnt.data_ptr(), max_topk,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, st)
     else:
-        p = (_at(where, "q", q, bf16, n // 2, dev),
-             _at(where, "block_idx", block_idx, i32, units * (max_topk + 1), dev),
-             _at(where, "block_cnt", block_cnt, i32, units, dev), max_topk,
-             _at(where, "out", out, f32, n, dev), _at(where, "lse", lse, f32, rows, dev))
-    st = lib().resa_sparse_decode_q4(_addr(cfg), _addr(cache), *p, ws.data_ptr(), ws.nbytes, st)
+        st = lib().resa_sparse_decode_q4(
+            _addr(cfg), _addr(cache), _at(where, "q", q, bf16, n // 2, dev),
+            _at(where, "block_idx", block_idx, i32, units * (max_topk + 1), dev),
+            _at(where, "block_cnt", block_cnt, i32, units, dev), max_topk,
+            _at(where, "out", out, f32, n, dev), _at(where, "lse", lse, f32, rows, dev),
+            ws.data_ptr(), ws.nbytes, st)
     if st != RESA_OK:
         raise ResaError(st, where)
 
