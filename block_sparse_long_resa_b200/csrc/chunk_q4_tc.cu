@@ -60,8 +60,11 @@ static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "registers of th
 constexpr int kPieceTiles = 8;          // tiles a CTA takes in the time that a second piece adds
 constexpr int kMinTiles = 2;            // tiles a CTA takes at least, when there are few
 constexpr int kChain = 2;               // tiles whose P V add up in tensor memory
-constexpr float kShift = 12.f;          // P is stored as 2^kShift * exp2(x - m)
-constexpr float kSlack = 3.f;           // growth of the maximum tolerated before rescaling
+// P is stored as 2^kShift * exp2(x - m), at most 2^(kShift + kSlack).  hi is cut off, not
+// rounded, to 11 bits, so a P below fp16's normal numbers is off by half a smallest step in hi
+// and another in lo, 2^-24: 2^-36 of the row's largest, which is at least 2^(kShift - 1).
+constexpr float kShift = 13.f;
+constexpr float kSlack = 2.f;           // growth of the maximum tolerated before rescaling
 
 template <int D>
 struct ChunkSmem {

@@ -198,3 +198,30 @@ def test_chunks_of_long_pieces_and_many_units(cuda_device, layout, lens, f):
             p.check(out, lse, q, i, h, fresh[i])
     o2, l2 = p.attention(f, q, fresh)
     assert np.array_equal(out, o2) and np.array_equal(lse, l2)
+
+
+@pytest.mark.parametrize("f", [1, 2])
+def test_small_weights_beside_a_large_one(cuda_device, f):
+    """Two keys, the first with nearly all the weight and values of zero: the output is the second's
+    weight times its values, down to the steps that a weight is stored in.  f = 2 is the chunk kernel
+    (24 rows a kv head)."""
+    n, hq, d = 400, 12, 64
+    p = Codes(340, [2] * n, hq, 1, d, 16, cuda_device, max_chunk=f)
+    first = p.table[:, 0]
+    p.k[first, 0, 0], p.k[first, 0, 1], p.v[first, 0, 0] = 0x77, 0x11, 0    # codes of 6, 0.5 and 0
+    p.ks[first, 0, :2] = 0x38                                               # times 1
+    for x, y in ((p.c4.tensors[0], p.k), (p.c4.tensors[1], p.ks), (p.c4.tensors[2], p.v)):
+        x.copy_(torch.from_numpy(y))
+    # logits of the first key from 14 to 24, a twelfth of that for the second
+    q = q4.bf16(p.rng.uniform(14, 24, (n, f, hq, 1)) / (6 * d ** 0.5) + np.zeros(d))
+    out, lse = p.attention(f, q)
+    k, v = zip(*((a, b) for a, b, _ in (p.keys_values(i, 0) for i in range(n))))
+    assert all((a[0] == 6).all() and (a[1] == 0.5).all() for a in k) and all((b[0] == 0).all() for b in v)
+    v = np.stack(v)[:, 1][:, None]                                          # [n, 1, d]
+    x = q[:, -1].sum(-1) * 6 * d ** -0.5
+    y = x * 11 / 12
+    want = (1 / (1 + np.exp(y)))[..., None] * v
+    # 2^-36 of the row's largest weight, which is 1 here; relatively as attention_tolerance has it
+    tol = np.abs(want) * (2 * 10 * 2.0 ** -22 * x[..., None] + 2.0 ** -20 + 2 * 65 * 2.0 ** -22)
+    assert (np.abs(out[:, -1] - want) <= tol + 2.0 ** -36 * np.abs(v)).all()
+    assert (np.abs(lse[:, -1] - (x + np.log1p(np.exp(-y)))) <= 10 * 2.0 ** -22 * x + 2.0 ** -20 + 65 * 2.0 ** -22).all()
