@@ -13,7 +13,7 @@
 // takes a token: its queries and its values.
 //
 // An angle is pos * inv_freq in turns in fp64, reduced to [-1/2, 1/2] before
-// the sine, so that a position of 2^20 has as good an angle as position 1.  Keys
+// the sine, so that the angle of a position of 2^20 is off by 2^-31 at most.  Keys
 // are rotated in fp64: their 4-bit codes are decisions, and an fp32 rotation
 // would move about one key in 10^4 to the neighbouring bf16 value.  (The fp64 result
 // is rounded to fp32 and then to bf16, which moves one in 10^5 that lies by a halfway

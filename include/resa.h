@@ -162,9 +162,9 @@ typedef struct {
  * head are rotated in pairs, the others are copied: with the token's position t
  * and a_i = t * inv_freq[i], pair i becomes
  *   (x1 cos a_i - x2 sin a_i, x2 cos a_i + x1 sin a_i) * mscale.
- * The angle is worked out and reduced in 64 bits, so that far positions have as good
- * angles as near ones; keys are rotated in 64 bits, rounded to fp32 and then to bf16,
- * queries in 32 bits and rounded to bf16. */
+ * The angle is worked out and reduced in 64 bits, off by |t * inv_freq| * 2^-51 at
+ * most; keys are rotated in 64 bits, rounded to fp32 and then to bf16, queries in 32
+ * bits and rounded to bf16. */
 typedef struct {
     int32_t rot_dim;       /* 0 .. d, a multiple of 16; 0: no rotation */
     int32_t interleaved;   /* 0: pair i = channels (i, i + rot_dim/2); 1: (2i, 2i+1) */
