@@ -34,7 +34,7 @@
 //
 // Measured (28 q / 4 kv heads, d 128, 32 rows against 4 x 65536 tokens: 120 GFLOP,
 // 1.5 times that in MMAs, 153 MB): 204 us, 0.59 PFLOP/s, 0.88 PFLOP/s in MMAs (185 us on
-// boxes that hold a higher clock under this load).
+// machines that hold a higher clock under this load).
 // Of a tile's 4900 cycles the chain of one M tile takes all: maximum 500, weights
 // 2600 (128 exponentials a thread at 4 a cycle and SM quarter are 1024), P V of the
 // second half 490, Q K^T 780.  An MMA with A in shared memory takes 97 cycles
